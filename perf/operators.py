@@ -165,8 +165,7 @@ def pack_records(kc, ke, vc, ve):
     v = vc.reshape(*lead, 2, 4, 2, dim // 64, 4, 2, 8)  # tokens: half, pair, odd; dim: 64s, 16s, 8s, 1s
     v = v.select(z + 2, 0) | (v.select(z + 2, 1) << 4)  # half, pair, 64s, 16s, 8s, 1s
     v = v.permute(*range(z), z + 2, z + 5, z + 1, z + 3, z + 0, z + 4).reshape(*lead, -1)
-    s = ve.reshape(*lead, 2, 4, 2, nb).permute(*range(z), z + 1, z + 3, z + 2, z + 0).reshape(*lead, -1)
-    return torch.cat([k, v, ke.reshape(*lead, -1), s], -1)
+    return torch.cat([k, v, ke.reshape(*lead, -1), ve.reshape(*lead, -1)], -1)
 
 
 def unpack_records(rec):
@@ -178,8 +177,7 @@ def unpack_records(rec):
     k = torch.stack([k & 15, k >> 4], -1).reshape(*lead, 16, dim)
     v = v.reshape(*lead, dim // 64, 8, 4, 4, 2, 2).permute(*range(z), z + 4, z + 2, z + 0, z + 3, z + 5, z + 1)  # half, pair, 64s, 16s, 8s, 1s
     v = torch.stack([v & 15, v >> 4], z + 2).reshape(*lead, 16, dim)
-    ve = ve.reshape(*lead, 4, nb, 2, 2).permute(*range(z), z + 3, z + 0, z + 2, z + 1).reshape(*lead, 16, nb)
-    return dequantize(k, ke.reshape(*lead, 16, nb)), dequantize(v, ve)
+    return dequantize(k, ke.reshape(*lead, 16, nb)), dequantize(v, ve.reshape(*lead, 16, nb))
 
 
 def read_cache(cache, table, kv_heads, dim, page):
@@ -384,7 +382,7 @@ def _stored(rec, dim):
     kbyte = tok * (dim // 2) + d % 32 // 8 * (dim // 8) + d // 32 * 4 + d % 8 // 2
     vbyte = 8 * dim + d // 64 * 512 + (d % 8 * 4 + pair) * 16 + d % 64 // 16 * 4 + half * 2 + d % 16 // 8
     kexp = 16 * dim + tok * (dim // 32) + d // 32
-    vexp = 16 * dim + dim // 2 + pair * (dim // 8) + d // 32 * 4 + odd * 2 + half
+    vexp = kexp + dim // 2
     values = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], device=DEV, dtype=torch.float64)
     out = []
     for byte, shift, ex in ((kbyte, d % 2 * 4 + 0 * tok, kexp), (vbyte, odd * 4 + 0 * d, vexp)):
