@@ -333,14 +333,114 @@ fp8mm_status concat_mla_k(const void* k_nope, const void* k_rope, void* k_out, i
                           int64_t nope_stride_t, int64_t nope_stride_h, int64_t rope_stride_t,
                           int64_t rope_stride_h, int64_t out_stride_t, int64_t out_stride_h, void* stream);
 
+/* ------------------------------------------- MXFP4 key/value cache in pages */
+
+/* Norm and rotation of queries and keys, the step between a QKV projection
+ * (fp8_gemm, mxfp8_gemm) and the cache; per head, in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * w             (left out when both weights are NULL)
+ *   (y[a], y[b]) <- (y[a] cos - y[b] sin, y[b] cos + y[a] sin)
+ * over rot_dim / 2 pairs, pair i being (i, i + rot_dim / 2), or with interleaved != 0 (2 i, 2 i + 1);
+ * elements from rot_dim on are not rotated.  fp32 throughout, rounded once to bf16.
+ *   q, k         [tokens, heads, head_dim] bf16, strides in elements (q and k may be slices of one
+ *                projection's output); q_out, k_out the same, and may be q and k themselves (in place); no
+ *                other overlap
+ *   q_weight, k_weight  [head_dim] bf16
+ *   cos_sin      [max_pos, rot_dim] fp32, row stride cos_sin_stride: rot_dim / 2 cosines, then the sines, of
+ *                each position (a table that the caller computes once, in 64 bits for far positions)
+ *   positions    [tokens] int32 device.  A negative one marks a padding row, which is left as it was; one
+ *                past the table is recorded in the device error word and the row left as it was.
+ * Requires head_dim 64, 128 or 256; rot_dim % 16 == 0, 16 <= rot_dim <= head_dim; 16-byte aligned pointers and
+ * strides.  tokens == 0 or no heads is a no-op. */
+fp8mm_status qk_norm_rope(const void* q_bf16, int64_t q_stride_t, int64_t q_stride_h, const void* k_bf16,
+                          int64_t k_stride_t, int64_t k_stride_h, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                          int64_t head_dim, const void* q_weight, const void* k_weight, float eps,
+                          const float* cos_sin, int64_t max_pos, int64_t rot_dim, int64_t cos_sin_stride,
+                          int32_t interleaved, const int32_t* positions, void* q_out, int64_t q_out_stride_t,
+                          int64_t q_out_stride_h, void* k_out, int64_t k_out_stride_t, int64_t k_out_stride_h,
+                          void* stream);
+
+/* A layer's key/value cache in pages, and the page table of a batch.
+ * Keys and values are MXFP4: E2M1 codes, one UE8M0 exponent e per 32 elements of the head dimension, value =
+ * code * 2^(e - 127), 4.25 bits per element.  e is the smallest with 6 * 2^(e - 127) >= the block's largest
+ * magnitude (0 for a block of zeros): mxfp8_quantize's rule with E2M1's largest value.
+ * A page holds page_size tokens of every head as [head][group of 16 tokens][record]; a record is 17 * head_dim
+ * bytes (key codes, value codes, key exponents, value exponents) in the order that the attention kernel's
+ * matrix instructions take; csrc/kv4.cuh has it byte by byte.  Token t of sequence s is in page
+ * page_table[s * table_stride + t / page_size].  Page ids are read only up to the sequence's length; ids
+ * outside [0, num_pages) are recorded in the device error word (kind 2) and neither read nor written through. */
+typedef struct fp8mm_kv_cache {
+  void* pages;               /* device, 16-byte aligned */
+  int64_t page_stride;       /* bytes from page to page: >= mxfp4_kv_page_bytes(...), a multiple of 16 */
+  int64_t num_pages;
+  int64_t page_size;         /* tokens: a multiple of 16, 16..4096 */
+  int64_t kv_heads;          /* 1..65535 */
+  int64_t head_dim;          /* 64 or 128 */
+  const int32_t* page_table; /* device [batch, max_pages], row stride table_stride elements */
+  int64_t table_stride;
+  int64_t max_pages;
+  int64_t batch;             /* sequences */
+} fp8mm_kv_cache;
+/* Bytes of a page; 0 for sizes that are not supported. */
+size_t mxfp4_kv_page_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim);
+
+/* Ragged batches (the next three calls): rows [cu_seqlens[s], cu_seqlens[s + 1]) belong to sequence s
+ * (int32 device, batch + 1 entries, cu_seqlens[0] >= 0, rising); cu_seqlens NULL means one row per sequence
+ * (rows == batch).  Rows behind cu_seqlens[batch] are padding: not read, and outputs left as they were.
+ * Bounds that do not fit are recorded in the device error word and their sequence skipped. */
+
+/* Quantizes new keys and values into the cache: sequence s's rows become its last tokens, positions
+ * seq_lens[s] - (rows of s) .. seq_lens[s] - 1, seq_lens (int32 device) counting them.  seq_lens[s] == 0
+ * marks a padding sequence.  Nothing but the new tokens' codes and exponents changes in a page (value codes
+ * share bytes between neighbouring tokens: of one page, only one call at a time may write).  Two sequences must
+ * not append into the same page.
+ *   k, v [rows, kv_heads, head_dim] bf16, strides in elements, 16-byte aligned. */
+fp8mm_status mxfp4_kv_append(const void* k_bf16, int64_t k_stride_t, int64_t k_stride_h, const void* v_bf16,
+                             int64_t v_stride_t, int64_t v_stride_h, int64_t rows, const int32_t* cu_seqlens,
+                             const int32_t* seq_lens, const fp8mm_kv_cache* cache, void* stream);
+
+/* Reads tokens back as bf16 (exact, but for magnitudes of 2^128, which become infinite): sequence s's rows are
+ * its tokens starts[s], starts[s] + 1, ... (starts NULL: from 0).  k, v [rows, kv_heads, head_dim] bf16 out. */
+fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts, const int32_t* cu_seqlens,
+                             int64_t rows, void* k_bf16, int64_t k_stride_t, int64_t k_stride_h, void* v_bf16,
+                             int64_t v_stride_t, int64_t v_stride_h, void* stream);
+
+/* Causal attention of the last tokens of each sequence over its cached keys and values:
+ *   out[r, h] = sum_j softmax_j(scale <q[r, h], k[j, h / g]>) v[j, h / g],  j <= position of row r,
+ * g = q_heads / kv_heads, row i of sequence s's n rows at position seq_lens[s] - n + i (append first, then
+ * attend).  A row that sees no token (seq_lens[s] == 0, or a position below 0) gives zeros.  Scores, softmax
+ * statistics and sums are fp32; queries enter exactly, weights with 11 bits.
+ *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned
+ *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
+ *        empty row
+ *   workspace  mxfp4_kv_attention_workspace_bytes(head_dim) bytes, 256-byte aligned, zeroed once before first
+ *        use; every call leaves its counters zero.  It lets long sequences be cut over the SMs.  Calls sharing one must
+ *        not overlap on the GPU.  NULL: a sequence and head is never cut.
+ * q must be finite.  Slots behind a sequence may hold any bytes. */
+fp8mm_status mxfp4_kv_attention(const void* q_bf16, int64_t q_stride_t, int64_t q_stride_h, int64_t rows,
+                                int64_t q_heads, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                const fp8mm_kv_cache* cache, float scale, void* out_bf16, int64_t out_stride_t,
+                                int64_t out_stride_h, float* lse, int64_t lse_stride, void* workspace,
+                                size_t workspace_bytes, void* stream);
+size_t mxfp4_kv_attention_workspace_bytes(int64_t head_dim);
+
+/* Copies whole pages, dst[i] <- src[i], in every layer: forking a sequence's partly filled last page, and
+ * compacting a pool.  src and dst are HOST arrays, taken by value (they may be freed when the call returns; a
+ * captured graph keeps them).  Every id in [0, num_pages), each dst at most once and none of them a src
+ * (FP8MM_ERR_SHAPE otherwise).
+ *   pages  device; page p of layer l at l * layer_stride + p * page_stride bytes; page_bytes are copied;
+ *          16-byte aligned, all three multiples of 16. */
+fp8mm_status kv_copy_pages(void* pages, int64_t num_pages, int64_t page_bytes, int64_t page_stride, int64_t layers,
+                           int64_t layer_stride, const int32_t* src, const int32_t* dst, int64_t moves, void* stream);
+
 /* ---------------------------------------------------------------- misc */
 
 const char* fp8mm_status_str(fp8mm_status status);
 /* CUDA error code of the last failed CUDA call made by the library (0 if none). */
 int fp8mm_last_cuda_error(void);
 /* Synchronizes the current device, returns the device error word (0 = none;
- * bits 0-7 kind (1 = bounded wait expired), 8-15 wait site, 16-31 CTA) and
- * clears it. */
+ * bits 0-7 kind (1 = bounded wait expired, 2 = an index in device memory out of
+ * range: site 16 a position, 17 a sequence's bounds or length, 18 a page id),
+ * 8-15 site, 16-31 CTA) and clears it. */
 unsigned int fp8mm_last_device_error(void);
 /* Self-test of the bounded wait: launches one CTA that waits on an mbarrier
  * nothing will ever arrive at, with a limit of timeout_us microseconds, and

@@ -35,4 +35,6 @@ from .fp8mm import (  # noqa: F401
     mxfp8_gemm, mxfp8_quantize, mxfp8_quantize_8x4, mxfp8_quantize_gemm, selftest_wait_timeout, sf_bytes,
     sf_from_canonical, sf_offset, sf_to_canonical, sf8x4_bytes, sf8x4_offset,
     pair_split_plan, quantize_gemm_workspace_bytes, version, workspace_bytes,
+    kv_copy_pages, mxfp4_kv_append, mxfp4_kv_attention, mxfp4_kv_attention_workspace_bytes, mxfp4_kv_gather,
+    mxfp4_kv_page_bytes, qk_norm_rope,
 )

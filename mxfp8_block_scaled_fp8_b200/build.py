@@ -11,15 +11,16 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libfp8mm.so")
-SOURCES = ["fp8mm.cu"]
-HEADERS = ["ptx.cuh", "quant.cuh", "gemm.cuh", "gemm2.cuh", "decode.cuh", "kvcache.cuh"]
+SOURCES = ["fp8mm.cu", "kv4.cu"]
+HEADERS = ["ptx.cuh", "quant.cuh", "gemm.cuh", "gemm2.cuh", "decode.cuh", "kvcache.cuh", "vec.cuh", "host.cuh", "kv4.cuh",
+           "kv4_attn.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-std=c++17", "-lineinfo",
     "-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-fmad=true",
     "-Xcompiler", "-fPIC", "-shared",
-    "-Xptxas", "-v",
+    "-Xptxas", "-v", "-t", "0",
 ]
 
 

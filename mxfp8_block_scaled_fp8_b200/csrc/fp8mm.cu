@@ -18,6 +18,7 @@
 #include "kvcache.cuh"
 #include "gemm.cuh"
 #include "gemm2.cuh"
+#include "host.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 
@@ -26,20 +27,14 @@ namespace fp8mm {
 // ------------------------------------------------------------------ host state
 static thread_local int t_last_cuda_error = 0;
 
-static fp8mm_status cuda_fail(cudaError_t e) {
+fp8mm_status cuda_fail(cudaError_t e) {
   t_last_cuda_error = static_cast<int>(e);
   return FP8MM_ERR_LAUNCH;
 }
 
-struct DeviceInfo {
-  int device = -1;
-  int sms = 0;
-  bool sm100 = false;
-};
-
 static std::mutex g_mu;
 
-static fp8mm_status current_device(DeviceInfo* info) {
+fp8mm_status current_device(DeviceInfo* info) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -61,7 +56,7 @@ static fp8mm_status current_device(DeviceInfo* info) {
 }
 
 // Opt a kernel into its dynamic shared memory size, once per device.
-static fp8mm_status ensure_smem(const void* kernel, int bytes, int dev) {
+fp8mm_status ensure_smem(const void* kernel, int bytes, int dev) {
   static std::set<std::pair<const void*, int>> done;
   std::lock_guard<std::mutex> lock(g_mu);
   if (done.count({kernel, dev})) return FP8MM_OK;
@@ -71,7 +66,7 @@ static fp8mm_status ensure_smem(const void* kernel, int bytes, int dev) {
   return FP8MM_OK;
 }
 
-static uint64_t wait_timeout_ns() {
+uint64_t wait_timeout_ns() {
   static uint64_t ns = [] {
     const char* s = std::getenv("FP8MM_WAIT_TIMEOUT_MS");
     long long ms = s ? std::atoll(s) : 0;
@@ -146,37 +141,6 @@ static bool make_c_map(CUtensorMap* map, void* c, int64_t m, int64_t n, int64_t 
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
-}
-
-static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Launch with programmatic stream serialisation (the kernel may begin while
-// the preceding kernel on the stream finishes; it waits for it in-kernel).
-template <typename... KArgs, typename... Args>
-static fp8mm_status launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                               Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  if (e != cudaSuccess) {
-    t_last_cuda_error = static_cast<int>(e);
-    return FP8MM_ERR_LAUNCH;
-  }
-  return FP8MM_OK;
-}
-
-static fp8mm_status launched() {
-  cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FP8MM_OK : cuda_fail(e);
 }
 
 // ------------------------------------------------------------------ kernels' configs
@@ -1081,7 +1045,8 @@ unsigned int fp8mm_last_device_error(void) {
   if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
   const unsigned int zero = 0;
   cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
-  return v;
+  const unsigned int kv = kv_take_device_error();
+  return v != 0 ? v : kv;
 }
 
 fp8mm_status fp8mm_selftest_wait_timeout(uint32_t timeout_us, void* stream) {

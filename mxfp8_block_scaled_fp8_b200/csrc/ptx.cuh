@@ -12,16 +12,20 @@
 namespace fp8mm {
 
 // ------------------------------------------------------------ error word
-// First device-side error since the last host read (0 = none).
+// First device-side error since the last host read (0 = none), one word per
+// translation unit.
 // Layout: bits 0..7 error kind, bits 8..15 wait site, bits 16..31 block id.
-__device__ unsigned int g_device_error = 0;
+static __device__ unsigned int g_device_error = 0;
 
-enum DevErr : unsigned { kDevErrTimeout = 1 };
+enum DevErr : unsigned { kDevErrTimeout = 1, kDevErrIndex = 2 };
 
 enum WaitSite : unsigned {
   kSiteProducerEmpty = 1, kSiteMmaFull = 2, kSiteMmaAccEmpty = 3, kSiteEpiAccFull = 4,
   kSiteDrain = 5, kSiteProducerDrain = 6, kSiteSelfTest = 7, kSiteEpiSync = 8, kSiteQuantStage = 9,
   kSiteClusterReduce = 10,
+  // data errors (kDevErrIndex): which index was out of range
+  kSitePosition = 16, kSiteSequence = 17, kSitePage = 18,
+  kSiteKvRecord = 19, kSiteKvDrain = 20,
 };
 
 __device__ __forceinline__ void record_error(unsigned kind, unsigned site) {
@@ -68,7 +72,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 
 // Bounded wait for the phase with the given parity to complete.  Returns
 // false when `timeout_ns` elapses or when another role raised `*abort`.
-__device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
                                             volatile int* abort, unsigned site) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
@@ -256,7 +260,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 }
 // Bounded wait with cluster-scope acquire (for barriers that receive arrivals
 // or transaction bytes from the peer CTA).
-__device__ __noinline__ bool mbar_wait_cluster_slow(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+static __device__ __noinline__ bool mbar_wait_cluster_slow(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
                                                     volatile int* abort, unsigned site) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
