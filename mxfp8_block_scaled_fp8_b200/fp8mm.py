@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -45,12 +46,9 @@ class Opts(ctypes.Structure):
                 ("kernel", ctypes.c_int32), ("small_m_ctas", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
-class KvCacheDesc(ctypes.Structure):
-    """fp8mm_kv_cache of the header."""
-    _fields_ = [("pages", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("num_pages", ctypes.c_int64),
-                ("page_size", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
-                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64),
-                ("batch", ctypes.c_int64)]
+# fp8mm_kv_cache of the header: pages, page_stride, num_pages, page_size, kv_heads, head_dim, page_table,
+# table_stride, max_pages, batch
+KV_CACHE_DESC = struct.Struct("@PqqqqqPqqq")
 
 
 _lib = None
@@ -69,9 +67,9 @@ _SIGNATURES = {
     "qk_norm_rope": ([_P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _I64, _I64,
                       _I64, ctypes.c_int32, _P, _P, _I64, _I64, _P, _I64, _I64, _P], ctypes.c_int),
     "mxfp4_kv_page_bytes": ([_I64, _I64, _I64], ctypes.c_size_t),
-    "mxfp4_kv_append": ([_P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, ctypes.POINTER(KvCacheDesc), _P], ctypes.c_int),
-    "mxfp4_kv_gather": ([ctypes.POINTER(KvCacheDesc), _P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P], ctypes.c_int),
-    "mxfp4_kv_attention": ([_P, _I64, _I64, _I64, _I64, _P, _P, ctypes.POINTER(KvCacheDesc), ctypes.c_float, _P, _I64,
+    "mxfp4_kv_append": ([_P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _P], ctypes.c_int),
+    "mxfp4_kv_gather": ([_P, _P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P], ctypes.c_int),
+    "mxfp4_kv_attention": ([_P, _I64, _I64, _I64, _I64, _P, _P, _P, ctypes.c_float, _P, _I64,
                             _I64, _P, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "mxfp4_kv_attention_workspace_bytes": ([_I64], ctypes.c_size_t),
     "kv_copy_pages": ([_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _P], ctypes.c_int),
@@ -384,47 +382,52 @@ def concat_mla_k(k_nope: torch.Tensor, k_rope: torch.Tensor, out: torch.Tensor |
 
 # ----------------------------------------------------------------- MXFP4 key/value cache in pages
 
-class _on:
-    """Runs a call on ``device`` and on ``stream`` (None: the device's current stream), whichever device is
-    current; what it allocates belongs to that stream.  ``raw`` is the stream's handle."""
-    __slots__ = ("ctx", "raw")
+# These calls run on the tensors' device and, with stream=None, on its current stream, whichever device is
+# current.  Their checks are written for a call every few microseconds: a decode step makes three per layer.
+_BF16, _I32, _F32, _BYTE = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_current, _raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, device, stream):
-        index = device.index
+
+class _on:
+    """Makes device ``index`` and ``stream`` (None: the device's current one) current, also for the allocator."""
+
+    def __init__(self, index: int, stream):
         if stream is not None and stream.device.index != index:
-            raise ValueError(f"stream of {stream.device}, tensors on {device}")
-        if stream is not None:
-            self.ctx, self.raw = torch.cuda.stream(stream), stream.cuda_stream
-        else:
-            self.ctx = torch.cuda.device(index) if torch.cuda.current_device() != index else None
-            self.raw = torch._C._cuda_getCurrentRawStream(index)
+            raise ValueError(f"stream of {stream.device}, tensors on cuda:{index}")
+        self.ctx = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw
+        return self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        return self.ctx.__exit__(*exc)
 
 
-def _tensor(t, dtype, device, name: str, shape=None, stride=None):
-    """Checks of one tensor argument: type, device, shape and unit stride of the last dimension."""
-    if t.dtype != dtype or t.device != device or device.type != "cuda":
-        raise TypeError(f"{name}: expected a CUDA {dtype} tensor on {device}, got {t.dtype} on {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+def _device(t: torch.Tensor, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise TypeError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return index
+
+
+def _tensor(t, dtype, index: int, name: str, shape=None, dims: int = 1):
+    """Checks of one tensor argument: type, device, shape (or dimensions), unit stride of the last dimension."""
+    if t.dtype is not dtype or t.get_device() != index:
+        raise TypeError(f"{name}: expected a {dtype} tensor on cuda:{index}, got {t.dtype} on {t.device}")
+    got = t.shape
+    if shape is not None and got != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(got)}")
+    if shape is None and len(got) != dims:
+        raise ValueError(f"{name}: expected {dims} dimensions, got shape {tuple(got)}")
+    if got[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: expected unit stride in the last dimension")
 
 
-def _heads(t, device, name: str):
-    """[rows, heads, dim] bf16 -> (pointer, row stride, head stride, the three sizes)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected [rows, heads, dim]")
-    _tensor(t, torch.bfloat16, device, name)
-    return (t.data_ptr(), t.stride(0), t.stride(1)), t.shape
+def _heads(t, index: int, name: str, shape=None):
+    """[rows, heads, dim] bf16 -> pointer, row stride, head stride."""
+    _tensor(t, _BF16, index, name, shape, 3)
+    st = t.stride()
+    return t.data_ptr(), st[0], st[1]
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: torch.Tensor, positions: torch.Tensor,
@@ -435,31 +438,32 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: torch.Tensor, positi
     q [T, q_heads, dim] and k [T, k_heads, dim] bf16 (strided views are taken): (q_out, k_out), new tensors unless
     given (q and k themselves: in place).  cos_sin [max_pos, rot] fp32: rot / 2 cosines, then the sines;
     positions int32 [T], negative for a padding row, which is left as it was."""
-    dev = q.device
-    qa, (t, hq, d) = _heads(q, dev, "q")
-    ka, (tk, hk, dk) = _heads(k, dev, "k")
+    dev = _device(q, "q")
+    if stream is not None or _current() != dev:
+        with _on(dev, stream):
+            return qk_norm_rope(q, k, cos_sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out)
+    qa, ka = _heads(q, dev, "q"), _heads(k, dev, "k")
+    (t, hq, d), (tk, hk, dk) = q.shape, k.shape
     if tk != t or dk != d:
         raise ValueError("q and k must have the same tokens and dim")
-    _tensor(cos_sin, torch.float32, dev, "cos_sin")
-    _tensor(positions, torch.int32, dev, "positions", (t,))
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin: expected [max_pos, rot]")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _tensor(w, torch.bfloat16, dev, name, (d,))
-    with _on(dev, stream) as raw:
-        if q_out is None:
-            q_out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
-        if k_out is None:
-            k_out = torch.empty((t, hk, d), dtype=torch.bfloat16, device=dev)
-        qo, qs = _heads(q_out, dev, "q_out")
-        ko, ks = _heads(k_out, dev, "k_out")
-        if qs != q.shape or ks != k.shape:
-            raise ValueError("q_out and k_out must have the shapes of q and k")
-        _check("qk_norm_rope", lib().qk_norm_rope(
-            *qa, *ka, t, hq, hk, d, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), eps, cos_sin.data_ptr(), cos_sin.shape[0],
-            cos_sin.shape[1], cos_sin.stride(0), 1 if interleaved else 0, positions.data_ptr(), *qo, *ko, raw))
+    _tensor(cos_sin, _F32, dev, "cos_sin", None, 2)
+    _tensor(positions, _I32, dev, "positions", (t,))
+    qw = kw = None
+    if q_weight is not None:
+        _tensor(q_weight, _BF16, dev, "q_weight", (d,))
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _tensor(k_weight, _BF16, dev, "k_weight", (d,))
+        kw = k_weight.data_ptr()
+    if q_out is None:
+        q_out = q.new_empty((t, hq, d))
+    if k_out is None:
+        k_out = k.new_empty((t, hk, d))
+    cs = cos_sin.shape
+    _check("qk_norm_rope", lib().qk_norm_rope(
+        *qa, *ka, t, hq, hk, d, qw, kw, eps, cos_sin.data_ptr(), cs[0], cs[1], cos_sin.stride(0),
+        1 if interleaved else 0, positions.data_ptr(), *_heads(q_out, dev, "q_out", q.shape),
+        *_heads(k_out, dev, "k_out", k.shape), _raw(dev)))
     return q_out, k_out
 
 
@@ -468,28 +472,18 @@ def mxfp4_kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
     return int(lib().mxfp4_kv_page_bytes(page_size, kv_heads, head_dim))
 
 
-def _kv_cache(cache, page_table, page_size: int, head_dim: int, device, kv_heads: int | None = None):
-    """The cache's description for the library (cache uint8 [pages, page_bytes], page_table int32 [batch, pages])."""
-    _tensor(cache, torch.uint8, device, "cache")
-    _tensor(page_table, torch.int32, device, "page_table")
-    if cache.dim() != 2 or page_table.dim() != 2:
-        raise ValueError("cache: expected [pages, page_bytes], page_table: [batch, pages]")
-    one = lib().mxfp4_kv_page_bytes(page_size, 1, head_dim)
-    if one == 0 or cache.shape[1] % one != 0 or cache.shape[1] == 0:
-        raise ValueError(f"cache: pages of {cache.shape[1]} bytes do not hold {page_size} tokens of whole heads of {head_dim}")
-    heads = cache.shape[1] // one
-    if kv_heads is not None and kv_heads != heads:
-        raise ValueError(f"cache: pages hold {heads} heads, not {kv_heads}")
-    return KvCacheDesc(cache.data_ptr(), cache.stride(0), cache.shape[0], page_size, heads, head_dim,
-                       page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
-                       page_table.shape[0])
-
-
-def _bounds(t, batch: int, device, name: str, more: int = 0):
-    if t is None:
-        return None
-    _tensor(t, torch.int32, device, name, (batch + more,))
-    return t.data_ptr()
+def _kv_cache(cache, page_table, page_size: int, head_dim: int, dev: int):
+    """(heads, batch, the cache's description for the library) of cache uint8 [pages, page_bytes] and page_table
+    int32 [batch, pages]."""
+    _tensor(cache, _BYTE, dev, "cache", None, 2)
+    _tensor(page_table, _I32, dev, "page_table", None, 2)
+    (pages, size), (batch, most) = cache.shape, page_table.shape
+    one = page_size // 16 * 17 * head_dim
+    if one <= 0 or size % one != 0 or size == 0:
+        raise ValueError(f"cache: pages of {size} bytes do not hold {page_size} tokens of whole heads of {head_dim}")
+    return size // one, batch, KV_CACHE_DESC.pack(
+        cache.data_ptr(), cache.stride(0), pages, page_size, size // one, head_dim, page_table.data_ptr(),
+        page_table.stride(0) if batch > 1 else most, most, batch)
 
 
 def mxfp4_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
@@ -498,16 +492,21 @@ def mxfp4_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_
     """Quantizes new keys and values [T, kv_heads, dim] bf16 into the MXFP4 cache uint8 [pages, page_bytes]: rows
     cu_seqlens[s]..cu_seqlens[s + 1] (None: row s) become the last tokens of sequence s, whose length with them
     is seq_lens[s] (int32; 0: a padding sequence).  Returns the cache."""
-    dev = cache.device
-    ka, (t, h, d) = _heads(k, dev, "k")
-    va, vs = _heads(v, dev, "v")
-    if vs != k.shape:
-        raise ValueError("k and v must have the same shape")
-    desc = _kv_cache(cache, page_table, page_size, d, dev, h)
-    cu = _bounds(cu_seqlens, desc.batch, dev, "cu_seqlens", 1)
-    lens = _bounds(seq_lens, desc.batch, dev, "seq_lens")
-    with _on(dev, stream) as raw:
-        _check("mxfp4_kv_append", lib().mxfp4_kv_append(*ka, *va, t, cu, lens, ctypes.byref(desc), raw))
+    dev = _device(cache, "cache")
+    if stream is not None or _current() != dev:
+        with _on(dev, stream):
+            return mxfp4_kv_append(k, v, cache, page_table, seq_lens, page_size, cu_seqlens)
+    ka, va = _heads(k, dev, "k"), _heads(v, dev, "v", k.shape)
+    t, h, d = k.shape
+    heads, batch, desc = _kv_cache(cache, page_table, page_size, d, dev)
+    if heads != h:
+        raise ValueError(f"cache: pages hold {heads} heads, not {h}")
+    cu = None
+    if cu_seqlens is not None:
+        _tensor(cu_seqlens, _I32, dev, "cu_seqlens", (batch + 1,))
+        cu = cu_seqlens.data_ptr()
+    _tensor(seq_lens, _I32, dev, "seq_lens", (batch,))
+    _check("mxfp4_kv_append", lib().mxfp4_kv_append(*ka, *va, t, cu, seq_lens.data_ptr(), desc, _raw(dev)))
     return cache
 
 
@@ -516,21 +515,23 @@ def mxfp4_kv_gather(cache: torch.Tensor, page_table: torch.Tensor, cu_seqlens: t
                     v: torch.Tensor | None = None, stream=None):
     """Cached keys and values as bf16 [total, kv_heads, head_dim] each: rows cu_seqlens[s]..cu_seqlens[s + 1] are
     the tokens of sequence s from starts[s] (None: 0) on."""
-    dev = cache.device
-    desc = _kv_cache(cache, page_table, page_size, head_dim, dev)
-    cu = _bounds(cu_seqlens, desc.batch, dev, "cu_seqlens", 1)
-    st = _bounds(starts, desc.batch, dev, "starts")
-    shape = (total, desc.kv_heads, head_dim)
-    with _on(dev, stream) as raw:
-        if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if v is None:
-            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        ka, ks = _heads(k, dev, "k")
-        va, vs = _heads(v, dev, "v")
-        if ks != shape or vs != shape:
-            raise ValueError(f"k and v must be {shape}")
-        _check("mxfp4_kv_gather", lib().mxfp4_kv_gather(ctypes.byref(desc), st, cu, total, *ka, *va, raw))
+    dev = _device(cache, "cache")
+    if stream is not None or _current() != dev:
+        with _on(dev, stream):
+            return mxfp4_kv_gather(cache, page_table, cu_seqlens, page_size, head_dim, total, starts, k, v)
+    heads, batch, desc = _kv_cache(cache, page_table, page_size, head_dim, dev)
+    _tensor(cu_seqlens, _I32, dev, "cu_seqlens", (batch + 1,))
+    st = None
+    if starts is not None:
+        _tensor(starts, _I32, dev, "starts", (batch,))
+        st = starts.data_ptr()
+    shape = (total, heads, head_dim)
+    if k is None:
+        k = cache.new_empty(shape, dtype=_BF16)
+    if v is None:
+        v = cache.new_empty(shape, dtype=_BF16)
+    _check("mxfp4_kv_gather", lib().mxfp4_kv_gather(desc, st, cu_seqlens.data_ptr(), total, *_heads(k, dev, "k", shape),
+                                                    *_heads(v, dev, "v", shape), _raw(dev)))
     return k, v
 
 
@@ -546,54 +547,62 @@ def mxfp4_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.T
     [T, q_heads, dim].  Rows cu_seqlens[s]..cu_seqlens[s + 1] (None: row s) stand at the last positions of
     sequence s, whose length is seq_lens[s]; scale None: dim ** -0.5.  lse: fp32 [T, q_heads] to fill.
     workspace (zeroed once, mxfp4_kv_attention_workspace_bytes(dim) bytes): lets long sequences be cut over the SMs."""
-    dev = cache.device
-    qa, (t, hq, d) = _heads(q, dev, "q")
-    desc = _kv_cache(cache, page_table, page_size, d, dev)
-    cu = _bounds(cu_seqlens, desc.batch, dev, "cu_seqlens", 1)
-    lens = _bounds(seq_lens, desc.batch, dev, "seq_lens")
+    dev = _device(cache, "cache")
+    if stream is not None or _current() != dev:
+        with _on(dev, stream):
+            return mxfp4_kv_attention(q, cache, page_table, seq_lens, page_size, cu_seqlens, scale, out, lse, workspace)
+    qa = _heads(q, dev, "q")
+    t, hq, d = q.shape
+    _, batch, desc = _kv_cache(cache, page_table, page_size, d, dev)
+    cu = lp = ws = None
+    lst = wsb = 0
+    if cu_seqlens is not None:
+        _tensor(cu_seqlens, _I32, dev, "cu_seqlens", (batch + 1,))
+        cu = cu_seqlens.data_ptr()
+    _tensor(seq_lens, _I32, dev, "seq_lens", (batch,))
     if lse is not None:
-        _tensor(lse, torch.float32, dev, "lse", (t, hq))
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        raise TypeError(f"workspace: expected a contiguous tensor on {dev}")
-    with _on(dev, stream) as raw:
-        if out is None:
-            out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
-        oa, os_ = _heads(out, dev, "out")
-        if os_ != q.shape:
-            raise ValueError("out must have the shape of q")
-        _check("mxfp4_kv_attention", lib().mxfp4_kv_attention(
-            *qa, t, hq, cu, lens, ctypes.byref(desc), d ** -0.5 if scale is None else scale, *oa,
-            None if lse is None else lse.data_ptr(), 0 if lse is None else lse.stride(0),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), raw))
+        _tensor(lse, _F32, dev, "lse", (t, hq))
+        lp, lst = lse.data_ptr(), lse.stride(0) if t > 1 else hq
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise TypeError(f"workspace: expected a contiguous tensor on cuda:{dev}")
+        ws, wsb = workspace.data_ptr(), workspace.nbytes
+    if out is None:
+        out = q.new_empty((t, hq, d))
+    _check("mxfp4_kv_attention", lib().mxfp4_kv_attention(
+        *qa, t, hq, cu, seq_lens.data_ptr(), desc, d ** -0.5 if scale is None else scale,
+        *_heads(out, dev, "out", q.shape), lp, lst, ws, wsb, _raw(dev)))
     return out
 
 
 def kv_copy_pages(cache: torch.Tensor, src, dst, stream=None) -> torch.Tensor:
     """Copies pages dst[i] <- src[i] (sequences or CPU tensors of page ids) in every layer of the cache
-    [pages, page_bytes] or [layers, pages, page_bytes] of any type.  No page may be written twice, or read and
-    written.  Returns the cache."""
-    dev = cache.device
-    if cache.dim() not in (2, 3) or not cache.is_cuda or (cache.stride(-1) != 1 and cache.shape[-1] > 1):
-        raise ValueError("cache: expected a CUDA tensor [pages, n] or [layers, pages, n] with unit stride in n")
+    [pages, n] or [layers, pages, n] of any type.  No page may be written twice, or read and written.
+    Returns the cache."""
+    dev = _device(cache, "cache")
+    if stream is not None or _current() != dev:
+        with _on(dev, stream):
+            return kv_copy_pages(cache, src, dst)
+    shape, st = cache.shape, cache.stride()
+    if len(shape) not in (2, 3) or (shape[-1] > 1 and st[-1] != 1):
+        raise ValueError("cache: expected [pages, n] or [layers, pages, n] with unit stride in n")
     n = len(src)
     if len(dst) != n:
         raise ValueError("src and dst must have the same length")
-    ids = (ctypes.c_int32 * (2 * n))(*_ids(src), *_ids(dst))
+    try:
+        ids = struct.pack(f"@{2 * n}i", *_ids(src), *_ids(dst))
+    except struct.error as e:
+        raise ValueError(f"page ids: {e}") from None
+    at = ctypes.cast(ids, _P).value
     size = cache.element_size()
-    layers, layer_stride = (cache.shape[0], cache.stride(0) * size) if cache.dim() == 3 else (1, 0)
-    with _on(dev, stream) as raw:
-        _check("kv_copy_pages", lib().kv_copy_pages(
-            cache.data_ptr(), cache.shape[-2], cache.shape[-1] * size, cache.stride(-2) * size, layers, layer_stride,
-            ids, ctypes.addressof(ids) + 4 * n, n, raw))
+    layers, layer_stride = (shape[0], st[0] * size) if len(shape) == 3 else (1, 0)
+    _check("kv_copy_pages", lib().kv_copy_pages(cache.data_ptr(), shape[-2], shape[-1] * size, st[-2] * size, layers,
+                                                layer_stride, at, at + 4 * n, n, _raw(dev)))
     return cache
 
 
 def _ids(x):
-    ids = x.tolist() if hasattr(x, "tolist") else list(x)
-    if any(not -2 ** 31 <= i < 2 ** 31 for i in ids):
-        raise ValueError("page ids must fit 32 bits")
-    return ids
+    return x.tolist() if hasattr(x, "tolist") else x
 
 
 # ----------------------------------------------------------------- misc
