@@ -127,8 +127,10 @@ fp8mm_status mxfp4_kv_append(const void* k_bf16, int64_t k_stride_t, int64_t k_s
   p.lens = seq_lens;
   p.batch = static_cast<int32_t>(cache->batch);
   p.rows = rows;
-  const int grid = kv_grid(rows * cache->kv_heads, kKvThreads, dev);
-  auto kern = cache->head_dim == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>;
+  const bool prompts = rows >= 8 * cache->batch;  // most groups have several new tokens
+  const int grid = kv_grid((prompts ? cdiv(rows, kGroup) : rows) * cache->kv_heads, kKvThreads, dev);
+  auto kern = prompts ? (cache->head_dim == 128 ? kv4_append_kernel<128, kGroup> : kv4_append_kernel<64, kGroup>)
+                      : (cache->head_dim == 128 ? kv4_append_kernel<128, 1> : kv4_append_kernel<64, 1>);
   st = launch_pdl(kern, dim3(grid), dim3(kKvThreads), 0, static_cast<cudaStream_t>(stream), p);
   return st != FP8MM_OK ? st : launched();
 }
@@ -157,8 +159,10 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
   p.starts = starts;
   p.batch = static_cast<int32_t>(cache->batch);
   p.rows = rows;
-  const int grid = kv_grid(rows * cache->kv_heads, kKvThreads, dev);
-  auto kern = cache->head_dim == 128 ? kv4_gather_kernel<128> : kv4_gather_kernel<64>;
+  const int grid = kv_grid(cdiv(rows, kGroup) * cache->kv_heads, kKvThreads, dev);
+  const bool wide = aligned(v_bf16, 32) && v_stride_t % 16 == 0 && v_stride_h % 16 == 0;
+  auto kern = cache->head_dim == 128 ? (wide ? kv4_gather_kernel<128, true> : kv4_gather_kernel<128, false>)
+                                     : (wide ? kv4_gather_kernel<64, true> : kv4_gather_kernel<64, false>);
   st = launch_pdl(kern, dim3(grid), dim3(kKvThreads), 0, static_cast<cudaStream_t>(stream), p);
   return st != FP8MM_OK ? st : launched();
 }
@@ -206,6 +210,7 @@ fp8mm_status mxfp4_kv_attention(const void* q_bf16, int64_t q_stride_t, int64_t 
   p.batch = static_cast<int32_t>(cache->batch);
   p.group = static_cast<int32_t>(q_heads / cache->kv_heads);
   p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  p.timeout_ns = wait_timeout_ns();
   const int grid = attn_ctas(dev.sms);
   if (workspace != nullptr) {
     p.counters = static_cast<unsigned*>(workspace);

@@ -156,50 +156,70 @@ struct KvAppendArgs {
 constexpr int kKvThreads = 128;
 
 // The rows of one 16-token group that a call touches.  A row leads the group
-// if it is its sequence's first new row or starts a group; the warp of the
+// if it is its sequence's first row or starts a group; the warp that has the
 // leading row handles the whole group, so that no two warps of a call write
 // into one record.
 struct KvSpan {
   int seq, group;
-  int first, end;      // token slots of the group that the call touches: [first, end)
-  int64_t row0;        // row of token slot `first`
+  int first, end;  // token slots of the group that the call touches: [first, end)
+  int row0;        // row of token slot `first`
 };
 
-// Span led by row r; false where the row leads none (or is not in the batch).
-// start: position of the sequence's first row.
-__device__ __forceinline__ bool kv_span(const int32_t* cu, int batch, int64_t rows, int64_t r, const int32_t* lens,
+// Rows r0 .. r0 + count - 1 (count <= 32, one per lane): true in the lanes
+// whose row leads a span.  lens: lengths with the rows; else starts (may be
+// nullptr: 0): positions of the sequences' first rows.
+__device__ __forceinline__ bool kv_span(const int32_t* cu, int batch, int rows, int r0, int count, const int32_t* lens,
                                         const int32_t* starts, KvSpan* sp) {
-  int seq, lo, n;
-  if (cu == nullptr) {
-    seq = static_cast<int>(r);
-    lo = seq;
-    n = 1;
-  } else {
-    const int end = cu[batch];
-    if (r >= min(static_cast<int64_t>(end), rows)) return false;  // behind the last sequence
-    seq = find_sequence(cu, batch, static_cast<int>(r));
+  const int r = r0 + (threadIdx.x & 31);
+  int seq = r, lo = r, n = 1;
+  if (cu != nullptr) {
+    const int end = min(cu[batch], rows);  // rows behind the last sequence are padding
+    if (r0 >= end) return false;
+    int a = find_sequence(cu, batch, r0);
+    int z = count == 1 ? a + 1 : find_sequence(cu, batch, min(r0 + count, end) - 1) + 1;
+    if (r >= end || r >= r0 + count) return false;
+    while (z - a > 1) {
+      const int mid = (a + z) / 2;
+      if (cu[mid] <= r) a = mid; else z = mid;
+    }
+    seq = a;
     lo = cu[seq];
-    n = cu[seq + 1] - lo;
-    if (lo < 0 || n < 1 || r < lo || r >= lo + static_cast<int64_t>(n) || lo + static_cast<int64_t>(n) > rows) {
+    const int64_t next = cu[seq + 1];
+    if (lo < 0 || r < lo || r >= next || next > rows) {
       record_index_error(kSiteSequence);
       return false;
     }
+    n = static_cast<int>(next) - lo;
+  } else if (r >= rows || r >= r0 + count) {
+    return false;
   }
-  // position of the first row: given, or the length (with the new rows) less their count
-  const int64_t start = lens != nullptr ? static_cast<int64_t>(lens[seq]) - n : (starts != nullptr ? starts[seq] : 0);
-  if (lens != nullptr && lens[seq] == 0) return false;  // a padding sequence: nothing of it is kept
+  int64_t start = starts != nullptr ? starts[seq] : 0;
+  if (lens != nullptr) {
+    if (lens[seq] == 0) return false;  // a padding sequence: nothing of it is kept
+    start = static_cast<int64_t>(lens[seq]) - n;
+  }
   if (start < 0 || start + n > INT32_MAX - kGroup) {
     record_index_error(kSiteSequence);
     return false;
   }
-  const int64_t pos = start + (r - lo);
+  const int pos = static_cast<int>(start) + (r - lo);
   if (r != lo && pos % kGroup != 0) return false;
   sp->seq = seq;
-  sp->group = static_cast<int>(pos / kGroup);
-  sp->first = static_cast<int>(pos % kGroup);
-  sp->end = static_cast<int>(min(static_cast<int64_t>(kGroup), start + n - static_cast<int64_t>(sp->group) * kGroup));
+  sp->group = pos / kGroup;
+  sp->first = pos % kGroup;
+  sp->end = min(kGroup, static_cast<int>(start) + n - pos / kGroup * kGroup);
   sp->row0 = r;
   return true;
+}
+// The span of lane `from`.
+__device__ __forceinline__ KvSpan span_of(const KvSpan& sp, int from) {
+  KvSpan o;
+  o.seq = __shfl_sync(0xFFFFFFFFu, sp.seq, from);
+  o.group = __shfl_sync(0xFFFFFFFFu, sp.group, from);
+  o.first = __shfl_sync(0xFFFFFFFFu, sp.first, from);
+  o.end = __shfl_sync(0xFFFFFFFFu, sp.end, from);
+  o.row0 = __shfl_sync(0xFFFFFFFFu, sp.row0, from);
+  return o;
 }
 
 // Quantizes a warp's group of keys or values.  Lane (g, c) = (lane / 4,
@@ -215,7 +235,7 @@ __device__ __forceinline__ void quantize_group(const __nv_bfloat16* x, int64_t s
   for (int h = 0; h < 2; ++h) {
     const int slot = g + 8 * h;
     const bool ok = slot >= sp.first && slot < sp.end;
-    const __nv_bfloat16* row = x + (sp.row0 + (slot - sp.first)) * st + 8 * c;
+    const __nv_bfloat16* row = x + (sp.row0 + static_cast<int64_t>(slot - sp.first)) * st + 8 * c;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
       v[h][b] = ok ? ld_stream_16(row + 32 * b) : make_uint4(0, 0, 0, 0);
@@ -253,77 +273,82 @@ __device__ __forceinline__ uint32_t load_exponents(const uint8_t* src) {
   return NB == 4 ? *reinterpret_cast<const uint32_t*>(src) : *reinterpret_cast<const uint16_t*>(src);
 }
 
-// One warp per (leading row, head).  Bound by HBM for long prompts (4 D bytes
+// One warp per (kRows rows, head): 1 where most rows lead a group (decode),
+// 16 for prompts.  Bound by HBM for long prompts (4 D bytes
 // in, 17 D / 16 bytes out per token and head) and by the latency of the index
 // loads for a decode step.  A group that is written only in part keeps the
 // codes of its other tokens: values share bytes between neighbouring tokens,
 // so those words are merged with what the record held.
-template <int D>
+template <int D, int kRows>
 __global__ void __launch_bounds__(kKvThreads) kv4_append_kernel(const KvAppendArgs p) {
   constexpr int NB = D / 32;
   __shared__ uint32_t s_code[kKvThreads / 32][kGroup][D / 8 + 4];
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t tasks = p.rows * p.kv.kv_heads;
+  const int blocks = static_cast<int>((p.rows + kRows - 1) / kRows);
+  const int64_t tasks = static_cast<int64_t>(blocks) * p.kv.kv_heads;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * (kKvThreads / 32);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kKvThreads / 32) + warp; t < tasks; t += stride) {
-    const int64_t r = t / p.kv.kv_heads;
-    const int head = static_cast<int>(t - r * p.kv.kv_heads);
-    KvSpan sp;
-    if (!kv_span(p.cu, p.batch, p.rows, r, p.lens, nullptr, &sp)) continue;
-    uint8_t* rec = kv_record<D>(p.kv, sp.seq, sp.group, head);
-    if (rec == nullptr) continue;
-    const int g = lane >> 2, c = lane & 3;
-    uint32_t code[2][NB], e[2][NB];
-    // keys: every token's codes and exponents are its own bytes
-    quantize_group<D>(p.k + head * p.k_sh, p.k_st, sp, lane, code, e);
+    const int block = static_cast<int>(t / p.kv.kv_heads);
+    const int head = static_cast<int>(t - static_cast<int64_t>(block) * p.kv.kv_heads);
+    KvSpan mine;
+    const bool leads = kv_span(p.cu, p.batch, static_cast<int>(p.rows), block * kRows, kRows, p.lens, nullptr, &mine);
+    for (unsigned todo = __ballot_sync(0xFFFFFFFFu, leads); todo != 0; todo &= todo - 1) {
+      const KvSpan sp = span_of(mine, __ffs(todo) - 1);
+      uint8_t* rec = kv_record<D>(p.kv, sp.seq, sp.group, head);
+      if (rec == nullptr) continue;
+      const int g = lane >> 2, c = lane & 3;
+      uint32_t code[2][NB], e[2][NB];
+      // keys: every token's codes and exponents are its own bytes
+      quantize_group<D>(p.k + head * p.k_sh, p.k_st, sp, lane, code, e);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int slot = g + 8 * h;
-      if (slot < sp.first || slot >= sp.end) continue;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(rec + slot * (D / 2) + c * (D / 8));
-      if constexpr (NB == 4)
-        *reinterpret_cast<uint4*>(dst) = make_uint4(code[h][0], code[h][1], code[h][2], code[h][3]);
-      else
-        *reinterpret_cast<uint2*>(dst) = make_uint2(code[h][0], code[h][1]);
-      if (c == 0) store_exponents<NB>(rec + 16 * D + slot * NB, e[h]);
-    }
-    // values: exponents by token, codes through shared memory and an 8 x 8 transpose
-    quantize_group<D>(p.v + head * p.v_sh, p.v_st, sp, lane, code, e);
-    __syncwarp();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int slot = g + 8 * h;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) s_code[warp][slot][4 * b + c] = code[h][b];
-      if (slot >= sp.first && slot < sp.end && c == 0) store_exponents<NB>(rec + 16 * D + D / 2 + slot * NB, e[h]);
-    }
-    __syncwarp();
-    if (lane < D / 4) {  // lane = (16-dimension slice j, pair cc)
-      const int j = lane & (D / 16 - 1), cc = lane / (D / 16);
-      uint32_t w[8];
-      uint32_t mask = 0;  // bits that the call writes
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {  // byte i / 2 = (half, d + 8), nibble i % 2: token 2 cc + i % 2 + 8 half
-        const int slot = 2 * cc + (i & 1) + 8 * (i >> 2);
-        w[i] = s_code[warp][slot][2 * j + ((i >> 1) & 1)];
-        if (slot >= sp.first && slot < sp.end) mask |= 0xFu << (4 * i);
+      for (int h = 0; h < 2; ++h) {
+        const int slot = g + 8 * h;
+        if (slot < sp.first || slot >= sp.end) continue;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(rec + slot * (D / 2) + c * (D / 8));
+        if constexpr (NB == 4)
+          *reinterpret_cast<uint4*>(dst) = make_uint4(code[h][0], code[h][1], code[h][2], code[h][3]);
+        else
+          *reinterpret_cast<uint2*>(dst) = make_uint2(code[h][0], code[h][1]);
+        if (c == 0) store_exponents<NB>(rec + 16 * D + slot * NB, e[h]);
       }
-      transpose_nibbles_8x8(w);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(rec + 8 * D + (j / 4) * 512 + cc * 16 + (j % 4) * 4);
-      if (mask == 0xFFFFFFFFu) {
+      // values: exponents by token, codes through shared memory and an 8 x 8 transpose
+      quantize_group<D>(p.v + head * p.v_sh, p.v_st, sp, lane, code, e);
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dst[16 * i] = w[i];
-      } else if (mask != 0) {
-        uint32_t old[8];
+      for (int h = 0; h < 2; ++h) {
+        const int slot = g + 8 * h;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) old[i] = dst[16 * i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dst[16 * i] = (old[i] & ~mask) | (w[i] & mask);
+        for (int b = 0; b < NB; ++b) s_code[warp][slot][4 * b + c] = code[h][b];
+        if (slot >= sp.first && slot < sp.end && c == 0) store_exponents<NB>(rec + 16 * D + D / 2 + slot * NB, e[h]);
       }
+      __syncwarp();
+      if (lane < D / 4) {  // lane = (16-dimension slice j, pair cc)
+        const int j = lane & (D / 16 - 1), cc = lane / (D / 16);
+        uint32_t w[8];
+        uint32_t mask = 0;  // bits that the call writes
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // byte i / 2 = (half, d + 8), nibble i % 2: token 2 cc + i % 2 + 8 half
+          const int slot = 2 * cc + (i & 1) + 8 * (i >> 2);
+          w[i] = s_code[warp][slot][2 * j + ((i >> 1) & 1)];
+          if (slot >= sp.first && slot < sp.end) mask |= 0xFu << (4 * i);
+        }
+        transpose_nibbles_8x8(w);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(rec + 8 * D + (j / 4) * 512 + cc * 16 + (j % 4) * 4);
+        if (mask == 0xFFFFFFFFu) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[16 * i] = w[i];
+        } else if (mask != 0) {
+          uint32_t old[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) old[i] = dst[16 * i];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[16 * i] = (old[i] & ~mask) | (w[i] & mask);
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
@@ -353,63 +378,81 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, float s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One warp per (leading row, head): the record's 17 D bytes in, 4 D bytes per
-// token out.  Bound by HBM (94 % of the bytes are the writes).
-template <int D>
+// 16 consecutive bf16 (32-byte store where the rows allow it).
+template <bool kWide>
+__device__ __forceinline__ void store_bf16x16(__nv_bfloat16* dst, const uint4& a, const uint4& b) {
+  if constexpr (kWide) {
+    st_global_v8(dst, a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w);
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = a;
+    reinterpret_cast<uint4*>(dst)[1] = b;
+  }
+}
+
+// One warp per (16 rows, head), 17 D bytes in, 4 D bytes per token out.
+// Bound by HBM (79 % of the bytes are the writes).  kWide: v's rows are
+// 32-byte aligned.
+template <int D, bool kWide>
 __global__ void __launch_bounds__(kKvThreads) kv4_gather_kernel(const KvGatherArgs p) {
   constexpr int NB = D / 32;
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t tasks = p.rows * p.kv.kv_heads;
+  const int g = lane >> 2, c = lane & 3;
+  const int j = lane & (D / 16 - 1), cc = (lane / (D / 16)) & 3;
+  const int blocks = static_cast<int>((p.rows + kGroup - 1) / kGroup);
+  const int64_t tasks = static_cast<int64_t>(blocks) * p.kv.kv_heads;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * (kKvThreads / 32);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kKvThreads / 32) + warp; t < tasks; t += stride) {
-    const int64_t r = t / p.kv.kv_heads;
-    const int head = static_cast<int>(t - r * p.kv.kv_heads);
-    KvSpan sp;
-    if (!kv_span(p.cu, p.batch, p.rows, r, nullptr, p.starts, &sp)) continue;
-    const uint8_t* rec = kv_record<D>(p.kv, sp.seq, sp.group, head);
-    if (rec == nullptr) continue;
-    const int g = lane >> 2, c = lane & 3;
-    uint32_t kw[2][NB], ke[2];
+    const int block = static_cast<int>(t / p.kv.kv_heads);
+    const int head = static_cast<int>(t - static_cast<int64_t>(block) * p.kv.kv_heads);
+    KvSpan mine;
+    const bool leads = kv_span(p.cu, p.batch, static_cast<int>(p.rows), block * kGroup, kGroup, nullptr, p.starts, &mine);
+    for (unsigned todo = __ballot_sync(0xFFFFFFFFu, leads); todo != 0; todo &= todo - 1) {
+      const KvSpan sp = span_of(mine, __ffs(todo) - 1);
+      const uint8_t* rec = kv_record<D>(p.kv, sp.seq, sp.group, head);
+      if (rec == nullptr) continue;
+      uint32_t kw[2][NB], ke[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* src = rec + (g + 8 * h) * (D / 2) + c * (D / 8);
-      if constexpr (NB == 4) {
-        const uint4 q = *reinterpret_cast<const uint4*>(src);
-        kw[h][0] = q.x, kw[h][1] = q.y, kw[h][2] = q.z, kw[h][3] = q.w;
-      } else {
-        const uint2 q = *reinterpret_cast<const uint2*>(src);
-        kw[h][0] = q.x, kw[h][1] = q.y;
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* src = rec + (g + 8 * h) * (D / 2) + c * (D / 8);
+        if constexpr (NB == 4) {
+          const uint4 q = *reinterpret_cast<const uint4*>(src);
+          kw[h][0] = q.x, kw[h][1] = q.y, kw[h][2] = q.z, kw[h][3] = q.w;
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(src);
+          kw[h][0] = q.x, kw[h][1] = q.y;
+        }
+        ke[h] = load_exponents<NB>(rec + 16 * D + (g + 8 * h) * NB);
       }
-      ke[h] = load_exponents<NB>(rec + 16 * D + (g + 8 * h) * NB);
-    }
-    const int j = lane & (D / 16 - 1), cc = (lane / (D / 16)) & 3;
-    uint32_t w[8], ve[4];  // ve: of tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9
-    const uint32_t* vsrc = reinterpret_cast<const uint32_t*>(rec + 8 * D + (j / 4) * 512 + cc * 16 + (j % 4) * 4);
+      uint32_t w[8], ve[4];  // ve: of tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9
+      const uint32_t* vsrc = reinterpret_cast<const uint32_t*>(rec + 8 * D + (j / 4) * 512 + cc * 16 + (j % 4) * 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = vsrc[16 * i];
+      for (int i = 0; i < 8; ++i) w[i] = vsrc[16 * i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ve[i] = rec[16 * D + D / 2 + (2 * cc + (i & 1) + 8 * (i >> 1)) * NB + j / 2];
+      for (int i = 0; i < 4; ++i) ve[i] = rec[16 * D + D / 2 + (2 * cc + (i & 1) + 8 * (i >> 1)) * NB + j / 2];
+      __nv_bfloat16* kd = p.k + head * p.k_sh + 8 * c;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int slot = g + 8 * h;
-      if (slot < sp.first || slot >= sp.end) continue;
-      __nv_bfloat16* dst = p.k + (sp.row0 + (slot - sp.first)) * p.k_st + head * p.k_sh + 8 * c;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        *reinterpret_cast<uint4*>(dst + 32 * b) = e2m1x8_to_bf16(kw[h][b], ue8m0_to_f32((ke[h] >> (8 * b)) & 0xFFu));
-    }
-    if (lane < D / 4) {
-      transpose_nibbles_8x8(w);  // w[i]: dimensions 16 j + 8 ((i / 2) % 2) + 0..7 of token 2 cc + i % 2 + 8 (i / 4)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int slot = 2 * cc + (i & 1) + 8 * (i >> 2);
+      for (int h = 0; h < 2; ++h) {
+        const int slot = g + 8 * h;
         if (slot < sp.first || slot >= sp.end) continue;
-        const uint32_t e = ve[(i & 1) + 2 * (i >> 2)];
-        __nv_bfloat16* dst = p.v + (sp.row0 + (slot - sp.first)) * p.v_st + head * p.v_sh + 16 * j + 8 * ((i >> 1) & 1);
-        *reinterpret_cast<uint4*>(dst) = e2m1x8_to_bf16(w[i], ue8m0_to_f32(e));
+        __nv_bfloat16* dst = kd + (sp.row0 + static_cast<int64_t>(slot - sp.first)) * p.k_st;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          *reinterpret_cast<uint4*>(dst + 32 * b) = e2m1x8_to_bf16(kw[h][b], ue8m0_to_f32((ke[h] >> (8 * b)) & 0xFFu));
+      }
+      if (lane < D / 4) {
+        transpose_nibbles_8x8(w);  // w[i]: dimensions 16 j + 8 ((i / 2) % 2) + 0..7 of token 2 cc + i % 2 + 8 (i / 4)
+        __nv_bfloat16* vd = p.v + head * p.v_sh + 16 * j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int slot = 2 * cc + (i & 1) + 8 * (i >> 1);
+          if (slot < sp.first || slot >= sp.end) continue;
+          const float f = ue8m0_to_f32(ve[i]);
+          const int at = 4 * (i >> 1) + (i & 1);
+          store_bf16x16<kWide>(vd + (sp.row0 + static_cast<int64_t>(slot - sp.first)) * p.v_st, e2m1x8_to_bf16(w[at], f),
+                               e2m1x8_to_bf16(w[at + 2], f));
+        }
       }
     }
   }

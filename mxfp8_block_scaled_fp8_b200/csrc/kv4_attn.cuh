@@ -45,12 +45,14 @@ struct KvAttnArgs {
   int64_t rows;
   int32_t batch, group;  // group: query heads per key/value head
   float scale_log2;      // scale * log2(e)
+  uint64_t timeout_ns;
   float* partials;       // nullptr: tiles are not cut
   unsigned* counters;    // one per CTA, zero between calls
 };
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnStages = 4;             // records of a warp's ring
 constexpr int kChunkGroups = kAttnWarps;  // groups of a chunk: one per warp
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -58,7 +60,9 @@ template <int D, int NT>
 struct AttnCfg {
   static constexpr int R = 8 * NT;
   static constexpr int kRowFloats = D + 4;  // padded row of a warp's partial result
-  static constexpr int kSmemBytes = kAttnWarps * R * (kRowFloats + 2) * 4;
+  static constexpr int kRecord = 17 * D;
+  static constexpr int kRingBytes = kAttnWarps * kAttnStages * kRecord;
+  static constexpr int kSmemBytes = kRingBytes + kAttnWarps * R * (kRowFloats + 2) * 4;
   static constexpr int kPartFloats = R * (D + 2);
 };
 
@@ -422,141 +426,248 @@ __device__ __forceinline__ void attn_store(const KvAttnArgs& p, const AttnSeq& q
 // Weight of a partial result with maximum m under the joint maximum mx.
 __device__ __forceinline__ float join_weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads) kv4_attn_kernel(const KvAttnArgs p) {
-  using Cfg = AttnCfg<D, NT>;
-  constexpr int R = Cfg::R, RF = Cfg::kRowFloats, NB = D / 32, NJ = D / 16;
-  extern __shared__ __align__(16) float smem[];
-  __shared__ AttnPlan plan;
-  float* so = smem;                               // [warps][R][RF]
-  float* sm = smem + kAttnWarps * R * RF;         // [warps][R]
-  float* sl = sm + kAttnWarps * R;                // [warps][R]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  griddep_launch_dependents();
-  griddep_wait();
+// A CTA's part of a tile: groups [g0, g1) of sequence s and one head.
+struct AttnPiece {
+  AttnSeq q;
+  int s, head, g0, g1;
+  int64_t base;             // units before sequence s
+  int64_t i0, i1, u, end;   // units of the tile; of the piece
+  int64_t row0;             // the tile's first row among the sequence's rows of a head
+};
 
-  const int per = attn_plan<R>(p, plan);
-  const int64_t total = plan.before[kAttnThreads];
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);  // each has at least one unit
-  if (blockIdx.x >= ctas) return;
-  int64_t u = blockIdx.x * total / ctas;
-  const int64_t u_begin = u, u1 = (blockIdx.x + 1) * total / ctas;
-  int s;
-  int64_t base;  // units before sequence s
-  {
-    int lo = 0, hi = kAttnThreads;  // before[lo] <= u < before[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (plan.before[mid] <= u) lo = mid; else hi = mid;
-    }
-    s = lo * per;
-    base = plan.before[lo];
+// The piece that begins at unit u (which [.., u1) contains), going on from
+// sequence pc.s.
+template <int R>
+__device__ __forceinline__ void attn_piece(const KvAttnArgs& p, AttnPiece& pc, int64_t u, int64_t u1) {
+  while (u >= pc.base + pc.q.tiles * pc.q.chunks) {
+    pc.base += pc.q.tiles * pc.q.chunks;
+    pc.q = attn_seq<R>(p, ++pc.s);
   }
-  AttnSeq q = attn_seq<R>(p, s);
-  AttnWarp<D, NT> w;
-  while (u < u1) {
-    while (u >= base + q.tiles * q.chunks) {
-      base += q.tiles * q.chunks;
-      q = attn_seq<R>(p, ++s);
-    }
-    const int64_t tile = (u - base) / q.chunks;
-    const int64_t i0 = base + tile * q.chunks, i1 = i0 + q.chunks;
-    const int head = static_cast<int>(tile % p.kv.kv_heads);
-    const int64_t row0 = tile / p.kv.kv_heads * R;
-    const int64_t end = min(u1, i1);
-    const int groups = (q.len + kGroup - 1) / kGroup;
-    int g0 = 0, g1 = groups;
-    if (p.partials != nullptr) {
-      g0 = static_cast<int>(u - i0) * kChunkGroups;
-      g1 = min(groups, static_cast<int>(end - i0) * kChunkGroups);
-    }
-    w.begin(p, q, row0, head);
-    g1 = min(g1, (max(w.vis_max, 0) + kGroup - 1) / kGroup);
-    for (int gi = g0 + warp; gi < g1; gi += kAttnWarps) {
-      const uint8_t* rec = kv_record<D>(p.kv, s, gi, head);
-      if (rec == nullptr) continue;
-      uint32_t kw[2][NB], ke[2], vw[NJ], ve[2];
+  const int64_t tile = (u - pc.base) / pc.q.chunks;
+  pc.i0 = pc.base + tile * pc.q.chunks;
+  pc.i1 = pc.i0 + pc.q.chunks;
+  pc.u = u;
+  pc.end = min(u1, pc.i1);
+  pc.head = static_cast<int>(tile % p.kv.kv_heads);
+  pc.row0 = tile / p.kv.kv_heads * R;
+  // groups up to the last row's position
+  const int64_t last = min(pc.row0 + R, static_cast<int64_t>(pc.q.n) * p.group) - 1;
+  const int seen = pc.q.len - pc.q.n + static_cast<int>(last / p.group) + 1;
+  pc.g0 = 0;
+  pc.g1 = (max(seen, 0) + kGroup - 1) / kGroup;
+  if (p.partials != nullptr) {
+    pc.g0 = static_cast<int>(u - pc.i0) * kChunkGroups;
+    pc.g1 = min(pc.g1, static_cast<int>(pc.end - pc.i0) * kChunkGroups);
+  }
+}
+
+// Joins the warps' results of a piece (in shared memory) and writes the tile's
+// rows, or the piece's partial result, and then the tile if this CTA is the
+// last of its contributors.
+template <int D, int NT>
+__device__ __forceinline__ void attn_join(const KvAttnArgs& p, const AttnPiece& pc, const float* so, const float* sm,
+                                          const float* sl, int& is_last, int64_t u_begin, int64_t ctas, int64_t total) {
+  using Cfg = AttnCfg<D, NT>;
+  constexpr int R = Cfg::R, RF = Cfg::kRowFloats;
+  const bool whole = pc.u == pc.i0 && pc.end == pc.i1;
+  const int64_t rows = static_cast<int64_t>(pc.q.n) * p.group;
+  float* part = nullptr;
+  if (!whole) part = p.partials + (2 * blockIdx.x + (pc.i0 >= u_begin ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
+  for (int i = threadIdx.x; i < R * D / 4; i += kAttnThreads) {
+    const int row = i / (D / 4), d4 = i % (D / 4);
+    float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t* kp = reinterpret_cast<const uint32_t*>(rec + (g + 8 * h) * (D / 2) + c * (D / 8));
+    for (int k = 0; k < kAttnWarps; ++k) mx = fmaxf(mx, sm[k * R + row]);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) kw[h][b] = kp[b];
-        ke[h] = load_exponents<NB>(rec + 16 * D + (g + 8 * h) * NB);
-        ve[h] = load_exponents<NB>(rec + 16 * D + D / 2 + (g + 8 * h) * NB);
+    for (int k = 0; k < kAttnWarps; ++k) {
+      const float f = join_weight(sm[k * R + row], mx);
+      const float4 v = *reinterpret_cast<const float4*>(so + (k * R + row) * RF + 4 * d4);
+      sum = fmaf(f, sl[k * R + row], sum);
+      acc[0] = fmaf(f, v.x, acc[0]);
+      acc[1] = fmaf(f, v.y, acc[1]);
+      acc[2] = fmaf(f, v.z, acc[2]);
+      acc[3] = fmaf(f, v.w, acc[3]);
+    }
+    if (whole) {
+      if (pc.row0 + row < rows) attn_store<D>(p, pc.q, pc.row0 + row, pc.head, d4, acc, mx, sum);
+    } else {
+      *reinterpret_cast<float4*>(part + row * D + 4 * d4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (d4 == 0) {
+        part[R * D + row] = mx;
+        part[R * D + R + row] = sum;
       }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        vw[j] = *reinterpret_cast<const uint32_t*>(rec + 8 * D + (j / 4) * 512 + lane * 16 + (j % 4) * 4);
-      w.group(kw, ke, vw, ve, gi * kGroup, q.len);
     }
-    w.publish(so + warp * R * RF, sm + warp * R, sl + warp * R);
-    __syncthreads();
-    const bool whole = u == i0 && end == i1;
-    const int64_t rows = static_cast<int64_t>(q.n) * p.group;
-    float* part = nullptr;
-    if (!whole) part = p.partials + (2 * blockIdx.x + (i0 >= u_begin ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
+  }
+  __syncthreads();
+  if (whole) return;
+  // CTA that holds unit x: the largest b with b * total / ctas <= x
+  const int64_t first = ((pc.i0 + 1) * ctas - 1) / total, last = (pc.i1 * ctas - 1) / total;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const unsigned before = atomicAdd(p.counters + first, 1u);
+    is_last = before == static_cast<unsigned>(last - first);
+    if (is_last) p.counters[first] = 0;  // as found, for the next call
+    __threadfence();
+  }
+  __syncthreads();
+  if (is_last) {
     for (int i = threadIdx.x; i < R * D / 4; i += kAttnThreads) {
       const int row = i / (D / 4), d4 = i % (D / 4);
+      if (pc.row0 + row >= rows) continue;
       float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < kAttnWarps; ++k) mx = fmaxf(mx, sm[k * R + row]);
-#pragma unroll
-      for (int k = 0; k < kAttnWarps; ++k) {
-        const float f = join_weight(sm[k * R + row], mx);
-        const float4 v = *reinterpret_cast<const float4*>(so + (k * R + row) * RF + 4 * d4);
-        sum = fmaf(f, sl[k * R + row], sum);
+      for (int64_t b = first; b <= last; ++b) {  // slot 1: the tile begins in that CTA
+        const float* pt = p.partials + (2 * b + (b == first ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
+        mx = fmaxf(mx, __ldcg(pt + R * D + row));
+      }
+      for (int64_t b = first; b <= last; ++b) {
+        const float* pt = p.partials + (2 * b + (b == first ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
+        const float f = join_weight(__ldcg(pt + R * D + row), mx);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + row * D + 4 * d4));
+        sum = fmaf(f, __ldcg(pt + R * D + R + row), sum);
         acc[0] = fmaf(f, v.x, acc[0]);
         acc[1] = fmaf(f, v.y, acc[1]);
         acc[2] = fmaf(f, v.z, acc[2]);
         acc[3] = fmaf(f, v.w, acc[3]);
       }
-      if (whole) {
-        if (row0 + row < rows) attn_store<D>(p, q, row0 + row, head, d4, acc, mx, sum);
-      } else {
-        *reinterpret_cast<float4*>(part + row * D + 4 * d4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        if (d4 == 0) {
-          part[R * D + row] = mx;
-          part[R * D + R + row] = sum;
-        }
-      }
+      attn_store<D>(p, pc.q, pc.row0 + row, pc.head, d4, acc, mx, sum);
     }
+  }
+  __syncthreads();
+}
+
+// A warp's ring of records, filled by bulk copies that its lane 0 issues.
+template <int D>
+struct AttnRing {
+  static constexpr int S = kAttnStages, kRecord = 17 * D;
+  uint8_t* buf;
+  uint64_t* bar;        // [S]
+  uint32_t phase;       // bit i: parity of stage i's next completion
+  uint32_t good;        // bit i: stage i's record exists
+  uint64_t addr;        // lane i: record of group first + 8 (window + i), 0 where the page table has none
+  int first, last;      // the piece's groups of this warp: first, first + 8, .. < last
+  int issued, taken;
+
+  // Records of 32 of the warp's groups, from the window's first.
+  __device__ __forceinline__ void look(const KvCache& kv, int seq, int head) {
+    const int gi = first + (issued + (threadIdx.x & 31)) * kAttnWarps;
+    addr = gi < last ? reinterpret_cast<uint64_t>(kv_record<D>(kv, seq, gi, head)) : 0;
+  }
+  __device__ __forceinline__ void issue(const KvCache& kv, int seq, int head) {
+    if (first + issued * kAttnWarps >= last) return;
+    if ((issued & 31) == 0) look(kv, seq, head);
+    const uint64_t src = __shfl_sync(0xFFFFFFFFu, addr, issued & 31);
+    const int st = issued % S;
+    good = (good & ~(1u << st)) | ((src != 0 ? 1u : 0u) << st);
+    if ((threadIdx.x & 31) == 0 && src != 0) {
+      mbar_arrive_expect_tx(bar + st, kRecord);
+      bulk_load(buf + st * kRecord, reinterpret_cast<const void*>(src), kRecord, bar + st);
+    }
+    ++issued;
+  }
+  __device__ __forceinline__ void begin(const KvCache& kv, const AttnPiece& pc) {
+    first = pc.g0 + (threadIdx.x >> 5);
+    last = pc.g1;
+    issued = taken = 0;
+    for (int i = 0; i < S; ++i) issue(kv, pc.s, pc.head);
+  }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(const KvAttnArgs p) {
+  using Cfg = AttnCfg<D, NT>;
+  constexpr int R = Cfg::R, RF = Cfg::kRowFloats, NB = D / 32, NJ = D / 16, S = kAttnStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ AttnPlan plan;
+  __shared__ uint64_t bars[kAttnWarps][S];
+  float* so = reinterpret_cast<float*>(smem + Cfg::kRingBytes);  // [warps][R][RF]
+  float* sm = so + kAttnWarps * R * RF;                          // [warps][R]
+  float* sl = sm + kAttnWarps * R;                               // [warps][R]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
+  if (threadIdx.x < kAttnWarps * S) mbar_init(&bars[0][0] + threadIdx.x, 1);
+  fence_mbar_init();
+  griddep_launch_dependents();
+  griddep_wait();
+
+  const int per = attn_plan<R>(p, plan);  // and makes the barriers' set-up visible to the CTA
+  const int64_t total = plan.before[kAttnThreads];
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);  // each has at least one unit
+  if (blockIdx.x >= ctas) return;
+  const int64_t u_begin = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
+  AttnPiece pc;
+  {
+    int lo = 0, hi = kAttnThreads;  // before[lo] <= u_begin < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (plan.before[mid] <= u_begin) lo = mid; else hi = mid;
+    }
+    pc.s = lo * per;
+    pc.base = plan.before[lo];
+    pc.q = attn_seq<R>(p, pc.s);
+  }
+  AttnRing<D> ring;
+  ring.buf = smem + warp * (S * Cfg::kRecord);
+  ring.bar = bars[warp];
+  ring.phase = 0;
+  bool dead = false;  // a wait expired: no further copies or waits
+  AttnWarp<D, NT> w;
+  attn_piece<R>(p, pc, u_begin, u1);
+  ring.begin(p.kv, pc);
+  while (true) {
+    w.begin(p, pc.q, pc.row0, pc.head);
+    for (int gi = ring.first; gi < ring.last && !dead; gi += kAttnWarps) {
+      const int st = ring.taken % S;
+      ++ring.taken;
+      if (!((ring.good >> st) & 1u)) {
+        ring.issue(p.kv, pc.s, pc.head);
+        continue;
+      }
+      if (!warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvRecord)) {
+        --ring.taken;
+        dead = true;
+        break;
+      }
+      ring.phase ^= 1u << st;
+      const uint8_t* rec = ring.buf + st * Cfg::kRecord;
+      uint32_t kw[2][NB], ke[2], vw[NJ], ve[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* kp = rec + h * 4 * D + lane * (D / 8);
+        if constexpr (NB == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(kp);
+          kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(kp);
+          kw[h][0] = v.x, kw[h][1] = v.y;
+        }
+        ke[h] = load_exponents<NB>(rec + 16 * D + (g + 8 * h) * NB);
+        ve[h] = load_exponents<NB>(rec + 16 * D + D / 2 + (g + 8 * h) * NB);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; j += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(rec + 8 * D + (j / 4) * 512 + lane * 16);
+        vw[j] = v.x, vw[j + 1] = v.y, vw[j + 2] = v.z, vw[j + 3] = v.w;
+      }
+      __syncwarp();  // the record is in registers: its stage is free
+      ring.issue(p.kv, pc.s, pc.head);
+      w.group(kw, ke, vw, ve, gi * kGroup, pc.q.len);
+    }
+    // the next piece's first records are on their way while this one is joined
+    const AttnPiece done = pc;
+    const bool more = pc.end < u1;
+    if (more) {
+      attn_piece<R>(p, pc, done.end, u1);
+      if (!dead) ring.begin(p.kv, pc);
+    }
+    w.publish(so + warp * R * RF, sm + warp * R, sl + warp * R);
     __syncthreads();
-    if (!whole) {
-      // CTA that holds unit x: the largest b with b * total / ctas <= x
-      const int64_t first = ((i0 + 1) * ctas - 1) / total, last = (i1 * ctas - 1) / total;
-      if (threadIdx.x == 0) {
-        __threadfence();
-        const unsigned before = atomicAdd(p.counters + first, 1u);
-        plan.last = before == static_cast<unsigned>(last - first);
-        if (plan.last) p.counters[first] = 0;  // as found, for the next call
-        __threadfence();
-      }
-      __syncthreads();
-      if (plan.last) {
-        for (int i = threadIdx.x; i < R * D / 4; i += kAttnThreads) {
-          const int row = i / (D / 4), d4 = i % (D / 4);
-          if (row0 + row >= rows) continue;
-          float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int64_t b = first; b <= last; ++b) {  // slot 1: the tile begins in that CTA
-            const float* pt = p.partials + (2 * b + (b == first ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
-            mx = fmaxf(mx, __ldcg(pt + R * D + row));
-          }
-          for (int64_t b = first; b <= last; ++b) {
-            const float* pt = p.partials + (2 * b + (b == first ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
-            const float f = join_weight(__ldcg(pt + R * D + row), mx);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + row * D + 4 * d4));
-            sum = fmaf(f, __ldcg(pt + R * D + R + row), sum);
-            acc[0] = fmaf(f, v.x, acc[0]);
-            acc[1] = fmaf(f, v.y, acc[1]);
-            acc[2] = fmaf(f, v.z, acc[2]);
-            acc[3] = fmaf(f, v.w, acc[3]);
-          }
-          attn_store<D>(p, q, row0 + row, head, d4, acc, mx, sum);
-        }
-      }
-      __syncthreads();
+    attn_join<D, NT>(p, done, so, sm, sl, plan.last, u_begin, ctas, total);
+    if (!more) break;
+  }
+  if (dead) {  // the copies in flight land before the CTA gives its shared memory back
+    for (; ring.taken < ring.issued; ++ring.taken) {
+      const int st = ring.taken % S;
+      if ((ring.good >> st) & 1u) warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvDrain);
     }
-    u = end;
   }
 }
 
