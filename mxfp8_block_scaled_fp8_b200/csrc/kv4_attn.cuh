@@ -52,8 +52,9 @@ struct KvAttnArgs {
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnStages = 4;             // records of a warp's ring
-constexpr int kChunkGroups = kAttnWarps;  // groups of a chunk: one per warp
+constexpr int kStep = 2;                        // groups that a warp takes at once
+constexpr int kAttnStages = 2;                  // steps of a warp's ring
+constexpr int kChunkGroups = kStep * kAttnWarps;  // groups of a chunk: one step per warp
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D, int NT>
@@ -61,7 +62,7 @@ struct AttnCfg {
   static constexpr int R = 8 * NT;
   static constexpr int kRowFloats = D + 4;  // padded row of a warp's partial result
   static constexpr int kRecord = 17 * D;
-  static constexpr int kRingBytes = kAttnWarps * kAttnStages * kRecord;
+  static constexpr int kRingBytes = kAttnWarps * kAttnStages * kStep * kRecord;
   static constexpr int kSmemBytes = kRingBytes + kAttnWarps * R * (kRowFloats + 2) * 4;
   static constexpr int kPartFloats = R * (D + 2);
 };
@@ -73,6 +74,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Transpose of an 8 x 8 matrix of 16-bit elements held by a warp (lane: row
 // lane / 4, columns 2 (lane % 4) and + 1).
@@ -164,6 +172,9 @@ __device__ __forceinline__ int attn_plan(const KvAttnArgs& p, AttnPlan& pl) {
 // ------------------------------------------------------------------ one warp's part of a tile
 
 constexpr float kSlack = 2.f;  // how far (log2) a score may pass the running maximum before that moves
+constexpr float kHead = 2.f;   // to so far above it
+constexpr int kSpare = 8;      // how far E_b may be above what the weights need, to take in the step's exponents
+constexpr int kMinRef = 13;    // so that 2^(127 + kBias - E_b) is finite
 constexpr int kBias = 12;      // weights enter the second product times 2^kBias: 2^(kSlack + 1 + kBias) < 2^16
 
 template <int D, int NT>
@@ -173,15 +184,17 @@ struct AttnWarp {
   float o[NT][NJ][4];          // O^T: rows d = 16 j + g (+ 8), columns 2 c (+ 1)
   uint32_t qf[NT][NB][4];      // query fragments: column g, elements 32 b + 8 c + 0..7
   float sc[NT][2], m[NT][2], l[NT][2];  // columns 2 c, 2 c + 1
-  int ref[NB];                 // E_b
+  float unit[NB];              // 2^(127 + kBias - E_b), which tells E_b (kMinRef and up)
   uint32_t ref_half;           // E_b / 2 in bytes, with the bytes' top bits set
   int vis[NT][2];              // tokens visible to columns 2 c, 2 c + 1; INT_MAX where the column is no row
   int vis_min, vis_max;        // over the tile's rows
 
-  __device__ __forceinline__ void pack_refs() {
-    ref_half = 0x80808080u;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) ref_half |= static_cast<uint32_t>(min(ref[b] >> 1, 127)) << (8 * b);
+  __device__ __forceinline__ int ref(int b) const {
+    return 254 + kBias - static_cast<int>(__float_as_uint(unit[b]) >> 23);
+  }
+  __device__ __forceinline__ void set_ref(int b, int e) {
+    unit[b] = __uint_as_float(static_cast<uint32_t>(254 + kBias - e) << 23);
+    ref_half = (b == 0 ? 0x80808080u : ref_half) | static_cast<uint32_t>(min(e >> 1, 127)) << (8 * b);
   }
 
   // Rows rho = row0 + column of the tile; sequence rows from q.lo.
@@ -235,76 +248,62 @@ struct AttnWarp {
         for (int k = 0; k < 4; ++k) o[t][j][k] = 0.f;
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) ref[b] = 0;
-    pack_refs();
+    for (int b = 0; b < NB; ++b) set_ref(b, kMinRef);
     const int64_t last = min(row0 + 8 * NT, rows) - 1;
     vis_min = q.len - q.n + static_cast<int>(row0 / p.group) + 1;
     vis_max = q.len - q.n + static_cast<int>(last / p.group) + 1;
   }
 
-  // One group: kw, vw its code words, ke / ve the exponent words of tokens g
-  // and g + 8; base: position of its first token; len: the sequence's length.
-  __device__ __forceinline__ void group(const uint32_t (&kw)[2][NB], const uint32_t (&ke)[2], const uint32_t (&vw)[NJ],
-                                        uint32_t (&ve)[2], int base, int len) {
-    float x[NT][4];
+  // Code words of this lane: keys of tokens g (h = 0) and g + 8; values.
+  static __device__ __forceinline__ void load_keys(const uint8_t* rec, int h, uint32_t (&kw)[NB]) {
+    const uint8_t* kp = rec + h * 4 * D + (threadIdx.x & 31) * (D / 8);
+    if constexpr (NB == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(kp);
+      kw[0] = v.x, kw[1] = v.y, kw[2] = v.z, kw[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(kp);
+      kw[0] = v.x, kw[1] = v.y;
+    }
+  }
+  static __device__ __forceinline__ void load_values(const uint8_t* rec, uint32_t (&vw)[NJ]) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[t][k] = 0.f;
+    for (int j = 0; j < NJ; j += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(rec + 8 * D + (j / 4) * 512 + (threadIdx.x & 31) * 16);
+      vw[j] = v.x, vw[j + 1] = v.y, vw[j + 2] = v.z, vw[j + 3] = v.w;
+    }
+  }
+  // 2^(byte b of w - 127) as fp32 bits (0 for a byte of 0).
+  static __device__ __forceinline__ float exp_byte(uint32_t w, int b) {
+    return __uint_as_float((b == 3 ? w >> 1 : w << (23 - 8 * b)) & 0x7F800000u);
+  }
+
+  // S^T of one group into x (not yet scaled).
+  __device__ __forceinline__ void scores(const uint8_t* rec, float (&x)[NT][4]) {
+    const int g = (threadIdx.x & 31) >> 2;
+    uint32_t k0w[NB], k1w[NB];
+    load_keys(rec, 0, k0w);
+    load_keys(rec, 1, k1w);
     // exponents one up (their factor 2 is in sc), so that 0 is no zero
-    const uint32_t k0 = ke[0] + 0x01010101u, k1 = ke[1] + 0x01010101u;
+    const uint32_t k0 = load_exponents<NB>(rec + 16 * D + g * NB) + 0x01010101u;
+    const uint32_t k1 = load_exponents<NB>(rec + 16 * D + (g + 8) * NB) + 0x01010101u;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       uint32_t a[4], a8[4];
-      e2m1x8_to_f16(kw[0][b], a);
-      e2m1x8_to_f16(kw[1][b], a8);
-      const float f0 = __uint_as_float(((k0 >> (8 * b)) & 0xFFu) << 23);
-      const float f1 = __uint_as_float(((k1 >> (8 * b)) & 0xFFu) << 23);
+      e2m1x8_to_f16(k0w[b], a);
+      e2m1x8_to_f16(k1w[b], a8);
+      const float f0 = exp_byte(k0, b), f1 = exp_byte(k1, b);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(d, a[0], a8[0], a[1], a8[1], qf[t][b][0], qf[t][b][1]);
+        float d[4];
+        mma_f16_zero(d, a[0], a8[0], a[1], a8[1], qf[t][b][0], qf[t][b][1]);
         mma_f16(d, a[2], a8[2], a[3], a8[3], qf[t][b][2], qf[t][b][3]);
-        x[t][0] = fmaf(d[0], f0, x[t][0]);
-        x[t][1] = fmaf(d[1], f0, x[t][1]);
-        x[t][2] = fmaf(d[2], f1, x[t][2]);
-        x[t][3] = fmaf(d[3], f1, x[t][3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[t][k] = b == 0 ? d[k] * (k < 2 ? f0 : f1) : fmaf(d[k], k < 2 ? f0 : f1, x[t][k]);
       }
-    }
-    bool slow = base + kGroup > vis_min;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[t][k] *= sc[t][k & 1];
-      slow |= fmaxf(x[t][0], x[t][2]) > m[t][0] + kSlack || fmaxf(x[t][1], x[t][3]) > m[t][1] + kSlack;
-    }
-    // e <= E_b + 1 in every byte, compared by halves; and no E_b past what 2^(e - E_b) needs as a normal fp32
-    const uint32_t fit = (ref_half - ((ve[0] >> 1) & 0x7F7F7F7Fu)) & (ref_half - ((ve[1] >> 1) & 0x7F7F7F7Fu));
-    slow |= (fit & 0x80808080u) != 0x80808080u;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) slow |= ref[b] > 126 + kBias;
-    if (__any_sync(0xFFFFFFFFu, slow)) {
-      group_slow(x, vw, ve, base, len);
-      return;
-    }
-    float pr[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) pr[t][k] = ex2(x[t][k] - m[t][k & 1]);
-      l[t][0] += pr[t][0] + pr[t][2];
-      l[t][1] += pr[t][1] + pr[t][3];
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t one = static_cast<uint32_t>(127 + kBias - ref[b]) << 23;
-      const float f0 = __uint_as_float((((ve[0] >> (8 * b)) & 0xFFu) << 23) + one);
-      const float f1 = __uint_as_float((((ve[1] >> (8 * b)) & 0xFFu) << 23) + one);
-      value_product(pr, vw, b, f0, f1);
     }
   }
 
-  // O^T += V_b^T (P f), f0 / f1 the factors of tokens g and g + 8.
+  // O^T += V_b^T (P f) for one group, f0 / f1 the factors of tokens g and g + 8.
   __device__ __forceinline__ void value_product(const float (&pr)[NT][4], const uint32_t (&vw)[NJ], int b, float f0,
                                                 float f1) {
     uint32_t v0[4], v1[4];
@@ -320,63 +319,150 @@ struct AttnWarp {
     }
   }
 
-  // The same with masks, a new maximum or new references.
-  __device__ __forceinline__ void group_slow(float (&x)[NT][4], const uint32_t (&vw)[NJ], uint32_t (&ve)[2], int base,
-                                             int len) {
+  // kStep groups at rec, rec + 17 D, from token position base on; good: bit u
+  // where group u is there (else its tokens count as unseen); len: the
+  // sequence's length.
+  __device__ __forceinline__ void step(const uint8_t* rec, uint32_t good, int base, int len) {
     const int g = (threadIdx.x & 31) >> 2;
-    // exponents of tokens behind the sequence may be anything: 0
-    if (base + g >= len) ve[0] = 0;
-    if (base + g + 8 >= len) ve[1] = 0;
-    float pr[NT][4], r[NT][2];
-    int top[2] = {-1000, -1000};  // exponents of the largest weights of tokens g and g + 8 (p < 2^top)
-    int drop = 1000;              // how far the references may fall: the maxima's least rise
+    float x[kStep][NT][4];
+    uint32_t ve[kStep][2];
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) scores(rec + u * 17 * D, x[u]);
+    // e <= E_b + 1 in every byte, compared by halves
+    uint32_t fit = 0x80808080u;
+#pragma unroll
+    for (int u = 0; u < kStep; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ve[u][h] = load_exponents<NB>(rec + u * 17 * D + 16 * D + D / 2 + (g + 8 * h) * NB);
+        fit &= ref_half - ((ve[u][h] >> 1) & 0x7F7F7F7Fu);
+      }
+    bool slow = fit != 0x80808080u || base + kStep * kGroup > vis_min || good != (1u << kStep) - 1;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+          x[u][t][k] *= sc[t][k];
+          x[u][t][k + 2] *= sc[t][k];
+          mx = fmaxf(mx, fmaxf(x[u][t][k], x[u][t][k + 2]));
+        }
+        slow |= mx > m[t][k] + kSlack;
+      }
+    if (__any_sync(0xFFFFFFFFu, slow)) {
+      step_slow(x, rec, ve, good, base, len);
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) {
+      uint32_t vw[NJ];
+      load_values(rec + u * 17 * D, vw);
+      float pr[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pr[t][k] = ex2(x[u][t][k] - m[t][k & 1]);
+        l[t][0] += pr[t][0] + pr[t][2];
+        l[t][1] += pr[t][1] + pr[t][3];
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        value_product(pr, vw, b, exp_byte(ve[u][0], b) * unit[b], exp_byte(ve[u][1], b) * unit[b]);
+    }
+  }
+
+  // The same with masks, a new maximum or new references.
+  __device__ __forceinline__ void step_slow(float (&x)[kStep][NT][4], const uint8_t* rec, uint32_t (&ve)[kStep][2],
+                                            uint32_t good, int base, int len) {
+    const int g = (threadIdx.x & 31) >> 2;
+    float r[NT][2];
+    int top[kStep][2];  // exponents of the largest weights of tokens g and g + 8 (p < 2^top)
+    int drop = 1000;    // how far the references may fall: the maxima's least rise
+#pragma unroll
+    for (int u = 0; u < kStep; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        top[u][h] = -1000;
+        // exponents of tokens behind the sequence may be anything: 0
+        if (base + kGroup * u + g + 8 * h >= len || !((good >> u) & 1u)) ve[u][h] = 0;
+      }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const bool row = vis[t][k] != INT_MAX;
-        if (base + g >= min(vis[t][k], len)) x[t][k] = -INFINITY;
-        if (base + g + 8 >= min(vis[t][k], len)) x[t][k + 2] = -INFINITY;
-        float mx = fmaxf(x[t][k], x[t][k + 2]);
+        const int end = min(vis[t][k], len);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kStep; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (base + kGroup * u + g + 8 * h >= end || !((good >> u) & 1u)) x[u][t][k + 2 * h] = -INFINITY;
+            mx = fmaxf(mx, x[u][t][k + 2 * h]);
+          }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-        const float mn = fmaxf(m[t][k], mx);
-        const bool same = m[t][k] == mn;
+        const bool same = !(mx > m[t][k] + kSlack);
+        const float mn = same ? m[t][k] : mx + kHead;
         r[t][k] = same ? 1.f : ex2(m[t][k] - mn);
         // a column that is no row, or has met nothing yet, holds no sum that the references must keep
         if (row && m[t][k] != -INFINITY) drop = min(drop, same ? 0 : static_cast<int>(fminf(mn - m[t][k], 1000.f)));
         m[t][k] = mn;
         const float at = mn == -INFINITY ? 0.f : mn;
-        pr[t][k] = ex2(x[t][k] - at);
-        pr[t][k + 2] = ex2(x[t][k + 2] - at);
-        l[t][k] = l[t][k] * r[t][k] + pr[t][k] + pr[t][k + 2];
+        l[t][k] *= r[t][k];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (row && pr[t][k + 2 * h] > 0.f)
-            top[h] = max(top[h], static_cast<int>(__float_as_uint(pr[t][k + 2 * h]) >> 23) - 126);
+        for (int u = 0; u < kStep; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float pr = ex2(x[u][t][k + 2 * h] - at);
+            x[u][t][k + 2 * h] = pr;
+            l[t][k] += pr;
+            if (row && pr > 0.f) top[u][h] = max(top[u][h], static_cast<int>(__float_as_uint(pr) >> 23) - 126);
+          }
       }
     drop = __reduce_min_sync(0xFFFFFFFFu, drop);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int e0 = static_cast<int>((ve[0] >> (8 * b)) & 0xFFu), e1 = static_cast<int>((ve[1] >> (8 * b)) & 0xFFu);
-      const int old = ref[b];
-      ref[b] = __reduce_max_sync(0xFFFFFFFFu, max(max(old - drop, 0), max(e0 + top[0], e1 + top[1])));
+      const int old = ref(b);
+      int e = max(old - drop, kMinRef), all = 0;
+#pragma unroll
+      for (int u = 0; u < kStep; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int one = static_cast<int>((ve[u][h] >> (8 * b)) & 0xFFu);
+          e = max(e, one + top[u][h]);
+          all = max(all, one);
+        }
+      e = __reduce_max_sync(0xFFFFFFFFu, e);
+      e = max(e, min(e + kSpare, __reduce_max_sync(0xFFFFFFFFu, all)));
+      set_ref(b, e);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float s0 = scale2(r[t][0], old - ref[b]), s1 = scale2(r[t][1], old - ref[b]);
+        const float s0 = scale2(r[t][0], old - e), s1 = scale2(r[t][1], old - e);
 #pragma unroll
         for (int j = 2 * b; j < 2 * b + 2; ++j)
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[t][j][k] *= (k & 1) ? s1 : s0;
       }
-      float pb[NT][4];  // weight * 2^(e - E_b) first, in two steps that neither overflow nor lose bits, then kBias
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) pb[t][k] = fminf(scale2(pr[t][k], (k < 2 ? e0 : e1) - ref[b]), 1.f);
-      value_product(pb, vw, b, static_cast<float>(1 << kBias), static_cast<float>(1 << kBias));
     }
-    pack_refs();
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) {
+      uint32_t vw[NJ];
+      load_values(rec + u * 17 * D, vw);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int e0 = static_cast<int>((ve[u][0] >> (8 * b)) & 0xFFu) - ref(b);
+        const int e1 = static_cast<int>((ve[u][1] >> (8 * b)) & 0xFFu) - ref(b);
+        float pb[NT][4];  // weight * 2^(e - E_b): at most 1 where the column is a row
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pb[t][k] = fminf(scale2(x[u][t][k], k < 2 ? e0 : e1), 1.f);
+        value_product(pb, vw, b, static_cast<float>(1 << kBias), static_cast<float>(1 << kBias));
+      }
+    }
   }
 
   // Results to shared memory: [R][kRowFloats] sums in real units, maxima and
@@ -402,7 +488,7 @@ struct AttnWarp {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             so[(8 * t + 2 * c + (k & 1)) * RF + 16 * j + g + 8 * (k >> 1)] =
-                scale2(o[t][j][k], ref[b] - 127 - kBias);
+                scale2(o[t][j][k], ref(b) - 127 - kBias);
       }
     }
   }
@@ -535,37 +621,39 @@ __device__ __forceinline__ void attn_join(const KvAttnArgs& p, const AttnPiece& 
   __syncthreads();
 }
 
-// A warp's ring of records, filled by bulk copies that its lane 0 issues.
+// A warp's ring of steps (kStep records each), filled by bulk copies that
+// its first lanes issue, one per record.
 template <int D>
 struct AttnRing {
-  static constexpr int S = kAttnStages, kRecord = 17 * D;
+  static constexpr int S = kAttnStages, kRecord = 17 * D, kLook = 32 / kStep;
   uint8_t* buf;
   uint64_t* bar;        // [S]
   uint32_t phase;       // bit i: parity of stage i's next completion
-  uint32_t good;        // bit i: stage i's record exists
-  uint64_t addr;        // lane i: record of group first + 8 (window + i), 0 where the page table has none
-  int first, last;      // the piece's groups of this warp: first, first + 8, .. < last
-  int issued, taken;
+  uint32_t good;        // bit kStep i + u: record u of stage i is there
+  uint64_t addr;        // lane kStep i + u: record u of the window's step i, 0 where there is none
+  int first, last;      // the piece's groups: this warp's steps begin at first, first + kChunkGroups, .. < last
+  int issued, taken;    // steps
 
-  // Records of 32 of the warp's groups, from the window's first.
-  __device__ __forceinline__ void look(const KvCache& kv, int seq, int head) {
-    const int gi = first + (issued + (threadIdx.x & 31)) * kAttnWarps;
-    addr = gi < last ? reinterpret_cast<uint64_t>(kv_record<D>(kv, seq, gi, head)) : 0;
-  }
   __device__ __forceinline__ void issue(const KvCache& kv, int seq, int head) {
-    if (first + issued * kAttnWarps >= last) return;
-    if ((issued & 31) == 0) look(kv, seq, head);
-    const uint64_t src = __shfl_sync(0xFFFFFFFFu, addr, issued & 31);
-    const int st = issued % S;
-    good = (good & ~(1u << st)) | ((src != 0 ? 1u : 0u) << st);
-    if ((threadIdx.x & 31) == 0 && src != 0) {
-      mbar_arrive_expect_tx(bar + st, kRecord);
-      bulk_load(buf + st * kRecord, reinterpret_cast<const void*>(src), kRecord, bar + st);
+    if (first + issued * kChunkGroups >= last) return;
+    const int lane = threadIdx.x & 31;
+    if (issued % kLook == 0) {  // look up the records of the next kLook steps
+      const int gi = first + (issued + lane / kStep) * kChunkGroups + lane % kStep;
+      addr = gi < last ? reinterpret_cast<uint64_t>(kv_record<D>(kv, seq, gi, head)) : 0;
     }
+    const uint64_t src = __shfl_sync(0xFFFFFFFFu, addr, issued % kLook * kStep + lane % kStep);
+    const int st = issued % S;
+    const uint32_t there = __ballot_sync(0xFFFFFFFFu, src != 0) & ((1u << kStep) - 1);
+    good = (good & ~(((1u << kStep) - 1) << (kStep * st))) | (there << (kStep * st));
+    if (lane == 0 && there != 0) mbar_arrive_expect_tx(bar + st, __popc(there) * kRecord);
+    __syncwarp();
+    if (lane < kStep && src != 0)
+      bulk_load(buf + (st * kStep + lane) * kRecord, reinterpret_cast<const void*>(src), kRecord, bar + st);
     ++issued;
   }
+  __device__ __forceinline__ uint32_t there(int st) const { return (good >> (kStep * st)) & ((1u << kStep) - 1); }
   __device__ __forceinline__ void begin(const KvCache& kv, const AttnPiece& pc) {
-    first = pc.g0 + (threadIdx.x >> 5);
+    first = pc.g0 + (threadIdx.x >> 5) * kStep;
     last = pc.g1;
     issued = taken = 0;
     for (int i = 0; i < S; ++i) issue(kv, pc.s, pc.head);
@@ -575,14 +663,14 @@ struct AttnRing {
 template <int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(const KvAttnArgs p) {
   using Cfg = AttnCfg<D, NT>;
-  constexpr int R = Cfg::R, RF = Cfg::kRowFloats, NB = D / 32, NJ = D / 16, S = kAttnStages;
+  constexpr int R = Cfg::R, RF = Cfg::kRowFloats, S = kAttnStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnPlan plan;
   __shared__ uint64_t bars[kAttnWarps][S];
   float* so = reinterpret_cast<float*>(smem + Cfg::kRingBytes);  // [warps][R][RF]
   float* sm = so + kAttnWarps * R * RF;                          // [warps][R]
   float* sl = sm + kAttnWarps * R;                               // [warps][R]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
+  const int warp = threadIdx.x >> 5;
   if (threadIdx.x < kAttnWarps * S) mbar_init(&bars[0][0] + threadIdx.x, 1);
   fence_mbar_init();
   griddep_launch_dependents();
@@ -605,51 +693,29 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv4_attn_kernel
     pc.q = attn_seq<R>(p, pc.s);
   }
   AttnRing<D> ring;
-  ring.buf = smem + warp * (S * Cfg::kRecord);
+  ring.buf = smem + warp * (S * kStep * Cfg::kRecord);
   ring.bar = bars[warp];
-  ring.phase = 0;
+  ring.phase = ring.good = 0;
   bool dead = false;  // a wait expired: no further copies or waits
   AttnWarp<D, NT> w;
   attn_piece<R>(p, pc, u_begin, u1);
   ring.begin(p.kv, pc);
   while (true) {
     w.begin(p, pc.q, pc.row0, pc.head);
-    for (int gi = ring.first; gi < ring.last && !dead; gi += kAttnWarps) {
+    for (int gi = ring.first; gi < ring.last && !dead; gi += kChunkGroups) {
       const int st = ring.taken % S;
-      ++ring.taken;
-      if (!((ring.good >> st) & 1u)) {
-        ring.issue(p.kv, pc.s, pc.head);
-        continue;
-      }
-      if (!warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvRecord)) {
-        --ring.taken;
-        dead = true;
-        break;
-      }
-      ring.phase ^= 1u << st;
-      const uint8_t* rec = ring.buf + st * Cfg::kRecord;
-      uint32_t kw[2][NB], ke[2], vw[NJ], ve[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* kp = rec + h * 4 * D + lane * (D / 8);
-        if constexpr (NB == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(kp);
-          kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(kp);
-          kw[h][0] = v.x, kw[h][1] = v.y;
+      const uint32_t there = ring.there(st);
+      if (there != 0) {
+        if (!warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvRecord)) {
+          dead = true;
+          break;
         }
-        ke[h] = load_exponents<NB>(rec + 16 * D + (g + 8 * h) * NB);
-        ve[h] = load_exponents<NB>(rec + 16 * D + D / 2 + (g + 8 * h) * NB);
+        ring.phase ^= 1u << st;
+        w.step(ring.buf + st * kStep * Cfg::kRecord, there, gi * kGroup, pc.q.len);
+        __syncwarp();  // the stage is free
       }
-#pragma unroll
-      for (int j = 0; j < NJ; j += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(rec + 8 * D + (j / 4) * 512 + lane * 16);
-        vw[j] = v.x, vw[j + 1] = v.y, vw[j + 2] = v.z, vw[j + 3] = v.w;
-      }
-      __syncwarp();  // the record is in registers: its stage is free
+      ++ring.taken;
       ring.issue(p.kv, pc.s, pc.head);
-      w.group(kw, ke, vw, ve, gi * kGroup, pc.q.len);
     }
     // the next piece's first records are on their way while this one is joined
     const AttnPiece done = pc;
@@ -666,7 +732,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv4_attn_kernel
   if (dead) {  // the copies in flight land before the CTA gives its shared memory back
     for (; ring.taken < ring.issued; ++ring.taken) {
       const int st = ring.taken % S;
-      if ((ring.good >> st) & 1u) warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvDrain);
+      if (ring.there(st) != 0) warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvDrain);
     }
   }
 }
