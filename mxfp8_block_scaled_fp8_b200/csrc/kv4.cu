@@ -75,21 +75,25 @@ static bool valid_moves(const int32_t* src, const int32_t* dst, int64_t moves, i
   return true;
 }
 
-template <int D, int NT>
-static fp8mm_status launch_attn(const KvAttnArgs& p, int grid, cudaStream_t s, int dev) {
-  using Cfg = AttnCfg<D, NT>;
-  auto kern = kv4_attn_kernel<D, NT>;
-  const fp8mm_status st = ensure_smem(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, dev);
-  if (st != FP8MM_OK) return st;
-  return launch_pdl(kern, dim3(grid), dim3(kAttnThreads), Cfg::kSmemBytes, s, p);
+// Jobs of an attention call with a workspace, and that workspace: counters,
+// the list of cut tiles (one may begin in each job), two partial tiles per job.
+static int attn_jobs(int sms) { return kAttnCtas * kAttnWarps * sms; }
+static size_t attn_list_bytes(int sms) { return (256 + attn_jobs(sms) * sizeof(AttnCut) + 255) / 256 * 256; }
+static size_t attn_workspace(int sms, int64_t d) {  // 8 rows a tile, or 16 of half as many jobs
+  return attn_list_bytes(sms) + static_cast<size_t>(attn_jobs(sms)) * 2 * 8 * (d + 2) * sizeof(float);
 }
 
-// CTAs that share the work of an attention call: two per SM.
-static int attn_ctas(int sms) { return 2 * sms; }
-constexpr int kMaxAttnRows = 16;
-static size_t attn_counter_bytes(int sms) { return (static_cast<size_t>(attn_ctas(sms)) * 4 + 255) / 256 * 256; }
-static size_t attn_workspace(int sms, int64_t d) {
-  return attn_counter_bytes(sms) + static_cast<size_t>(attn_ctas(sms)) * 2 * kMaxAttnRows * (d + 2) * sizeof(float);
+template <int D, int NT, int FOLD>
+static fp8mm_status launch_attn(const KvAttnArgs& p, cudaStream_t s, const DeviceInfo& dev) {
+  using Cfg = AttnCfg<D, NT, FOLD>;
+  auto kern = kv4_attn_kernel<D, NT, FOLD>;
+  const int grid = (NT == 1 ? kAttnCtas : 1) * dev.sms;
+  const int smem = kAttnWarps * static_cast<int>(sizeof(AttnShared<D, NT, FOLD>));
+  fp8mm_status st = ensure_smem(reinterpret_cast<const void*>(kern), smem, dev.device);
+  if (st != FP8MM_OK) return st;
+  st = launch_pdl(kern, dim3(grid), dim3(kAttnThreads), smem, s, p);
+  if (st != FP8MM_OK || p.partials == nullptr) return st;
+  return launch_pdl(kv4_attn_join_kernel<D, Cfg::R>, dim3(2 * dev.sms), dim3(kJoinThreads), 0, s, p);
 }
 
 }  // namespace fp8mm
@@ -211,18 +215,29 @@ fp8mm_status mxfp4_kv_attention(const void* q_bf16, int64_t q_stride_t, int64_t 
   p.group = static_cast<int32_t>(q_heads / cache->kv_heads);
   p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
   p.timeout_ns = wait_timeout_ns();
-  const int grid = attn_ctas(dev.sms);
   if (workspace != nullptr) {
-    p.counters = static_cast<unsigned*>(workspace);
-    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_counter_bytes(dev.sms));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.counters = reinterpret_cast<AttnCounters*>(ws);
+    p.cuts = reinterpret_cast<AttnCut*>(ws + 256);
+    p.partials = reinterpret_cast<float*>(ws + attn_list_bytes(dev.sms));
   }
-  // rows that a sequence has on average decide the tile: 8 or 16 of them
-  const bool wide = cdiv(rows, cache->batch) * p.group > 8;
+  if (rows * p.group > INT32_MAX) return FP8MM_ERR_SHAPE;
+  // units: every tile's steps and layout, at most; more steps a unit where they would not fit 31 bits
+  const double steps = static_cast<double>(p.kv.max_pages) * p.kv.page_groups / kStep + 1 + kTileSteps;
+  const double tiles = (static_cast<double>(rows) * p.group / 4 + p.batch) * p.kv.kv_heads;
+  if (tiles > 1e9) return FP8MM_ERR_SHAPE;
+  p.unit_steps = static_cast<int32_t>(std::min(1e9, 1 + steps * tiles / 2e9));
+  // rows that a sequence has on average decide the tile: 4, 8 or 16 of them
+  const int64_t tile = cdiv(rows, cache->batch) * p.group;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 128)
-    st = wide ? launch_attn<128, 2>(p, grid, s, dev.device) : launch_attn<128, 1>(p, grid, s, dev.device);
+    st = tile <= 4   ? launch_attn<128, 1, 2>(p, s, dev)
+         : tile <= 8 ? launch_attn<128, 1, 1>(p, s, dev)
+                     : launch_attn<128, 2, 1>(p, s, dev);
   else
-    st = wide ? launch_attn<64, 2>(p, grid, s, dev.device) : launch_attn<64, 1>(p, grid, s, dev.device);
+    st = tile <= 4   ? launch_attn<64, 1, 2>(p, s, dev)
+         : tile <= 8 ? launch_attn<64, 1, 1>(p, s, dev)
+                     : launch_attn<64, 2, 1>(p, s, dev);
   return st != FP8MM_OK ? st : launched();
 }
 

@@ -5,14 +5,21 @@
 // sequence, over the keys k_j and values v_j of its key/value head, j <= t:
 //   s_j = scale * <q, k_j>,  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m).
 //
-// Work split.  A tile is R = 8 NT rows (query tokens x the heads that share a
-// key/value head) of one sequence and head; its cost is the sequence's length
-// in chunks.  All tiles' chunks stand in one line, which is cut into equal
-// parts, one per CTA, whatever the lengths; a tile that is cut leaves partial
-// results (unnormalised sum, maximum, sum of weights), which the CTA that
-// arrives last at the tile's counter joins in a fixed order.  The plan is
-// made on the device from the lengths, so nothing depends on a length that the
-// host guessed, and a captured graph follows the lengths in memory.
+// Work split.  A tile is R rows (4, 8 or 16; query tokens x the heads that
+// share a key/value head) of one sequence and head; its cost is the sequence's
+// length in steps of 32 tokens.  All tiles' steps stand in one line, which is
+// cut into equal jobs, whatever the lengths, and every warp works on its own
+// job: it lays out its tile, fills its own ring of records by bulk copies and
+// keeps its own softmax, with no barrier in the CTA after the plan.  A job's
+// part of one tile is a piece.  A tile that is cut leaves partial results
+// (unnormalised sum, maximum, sum of weights) and a line in a list, by which a
+// second kernel joins them in the order of the jobs.  The plan is made on the
+// device from the lengths, so nothing depends on a length that the host
+// guessed, and a captured graph follows the lengths in memory.
+// Measured on the way (4 contexts of 100003..131072 tokens, 8 heads): eight
+// warps of a CTA on one piece, joined through shared memory, 117 us; the same
+// with a warp that brings the records and one that joins results, 122 us (a
+// CTA waits for its slowest warp).
 //
 // Arithmetic.  Keys and values stay in registers as the record holds them.
 // E2M1 -> f16 is one exact conversion per two codes; a 16-token group is the
@@ -46,24 +53,37 @@ struct KvAttnArgs {
   int32_t batch, group;  // group: query heads per key/value head
   float scale_log2;      // scale * log2(e)
   uint64_t timeout_ns;
-  float* partials;       // nullptr: tiles are not cut
-  unsigned* counters;    // one per CTA, zero between calls
+  float* partials;       // two per job; nullptr: tiles are not cut
+  struct AttnCut* cuts;  // of the tiles that are cut
+  struct AttnCounters* counters;
+  int32_t unit_steps;    // steps of a unit: 1, or more where the units would not fit 31 bits
 };
 
-constexpr int kAttnWarps = 8;
+constexpr int kAttnCtas = 2;      // CTAs of an SM (NT = 1)
+constexpr int kAttnWarps = 8;     // of a CTA
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kStep = 2;                        // groups that a warp takes at once
-constexpr int kAttnStages = 2;                  // steps of a warp's ring
-constexpr int kChunkGroups = kStep * kAttnWarps;  // groups of a chunk: one step per warp
+constexpr int kStep = 2;          // groups that a warp takes at once
+constexpr int kAttnStages = 2;    // steps of a warp's ring
+
+// Zero between calls.
+struct AttnCounters {
+  unsigned cut, done;
+};
+// A tile that is cut over jobs first..last: rows row0.. of a head, of the
+// sequence whose rows begin at lo.
+struct AttnCut {
+  int32_t first, last, lo, head, row0, rows;
+};
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <int D, int NT>
+// NT tiles of 8 columns.  FOLD = 2 where a tile has at most four rows: its
+// rows stand twice in the eight columns, and columns 4..7 take the second of
+// two groups, so that softmax and weights have no idle columns.
+template <int D, int NT, int FOLD>
 struct AttnCfg {
-  static constexpr int R = 8 * NT;
-  static constexpr int kRowFloats = D + 4;  // padded row of a warp's partial result
+  static constexpr int R = 8 * NT / FOLD;  // rows of a tile
   static constexpr int kRecord = 17 * D;
-  static constexpr int kRingBytes = kAttnWarps * kAttnStages * kStep * kRecord;
-  static constexpr int kSmemBytes = kRingBytes + kAttnWarps * R * (kRowFloats + 2) * 4;
+  static constexpr int kRingBytes = kAttnStages * kStep * kRecord;  // of a warp
   static constexpr int kPartFloats = R * (D + 2);
 };
 
@@ -109,10 +129,14 @@ __device__ __forceinline__ float scale2(float x, int n) {
 
 // ------------------------------------------------------------------ the plan
 
+// What laying a tile out costs a warp, in steps (each short tile of a batch
+// adds its latency: queries, page table, first records, results).
+constexpr int kTileSteps = 4;
+
 struct AttnSeq {
   int lo, n, len;
-  int64_t tiles;   // row tiles x heads
-  int64_t chunks;  // of one tile
+  uint32_t tiles;  // row tiles x heads
+  uint32_t units;  // of one tile; the first ones stand for its layout
 };
 
 template <int R>
@@ -125,49 +149,60 @@ __device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs& p, int s) {
     q.n = 0;
   }
   q.len = p.lens[s];
-  const int64_t most = static_cast<int64_t>(p.kv.max_pages) * p.kv.page_groups * kGroup;
+  const int most = p.kv.max_pages * p.kv.page_groups * kGroup;  // fits: checked on the host
   if (q.len < 0 || q.len > most) {
     record_index_error(kSiteSequence);
-    q.len = q.len < 0 ? 0 : static_cast<int>(most);
+    q.len = max(0, min(q.len, most));
   }
-  q.tiles = (static_cast<int64_t>(q.n) * p.group + R - 1) / R * p.kv.kv_heads;
-  constexpr int kChunk = kChunkGroups * kGroup;
-  q.chunks = p.partials == nullptr ? 1 : max(1, (q.len + kChunk - 1) / kChunk);
+  // rows of a head below 2^31: checked on the host
+  q.tiles = (static_cast<uint32_t>(q.n) * p.group + R - 1) / R * p.kv.kv_heads;
+  const uint32_t steps = (static_cast<uint32_t>(q.len) + kStep * kGroup - 1) / (kStep * kGroup) + kTileSteps;
+  q.units = p.unit_steps == 1 ? steps : (steps + p.unit_steps - 1) / p.unit_steps;
+  if (p.partials == nullptr) q.units = 1;
   return q;
 }
 
 // Units before each strip of sequences; strip i is [i * per, (i + 1) * per).
 struct AttnPlan {
-  int64_t before[kAttnThreads + 1];
-  int64_t warp_sum[kAttnWarps];
-  int last;
+  uint32_t before[kAttnThreads + 1];
+  uint32_t warp_sum[kAttnWarps];
 };
 
 template <int R>
 __device__ __forceinline__ int attn_plan(const KvAttnArgs& p, AttnPlan& pl) {
   const int per = (p.batch + kAttnThreads - 1) / kAttnThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t mine = 0;
+  uint32_t sum = 0;
   const int s1 = min(p.batch, static_cast<int>((threadIdx.x + 1) * per));
   for (int s = threadIdx.x * per; s < s1; ++s) {
     const AttnSeq q = attn_seq<R>(p, s);
-    mine += q.tiles * q.chunks;
+    sum += q.tiles * q.units;
   }
-  int64_t sum = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
     if (lane >= o) sum += v;
   }
   if (lane == 31) pl.warp_sum[warp] = sum;
   __syncthreads();
-  int64_t base = 0;
-  for (int w = 0; w < warp; ++w) base += pl.warp_sum[w];
-  pl.before[threadIdx.x + 1] = base + sum;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) sum += w < warp ? pl.warp_sum[w] : 0u;
+  pl.before[threadIdx.x + 1] = sum;
   if (threadIdx.x == 0) pl.before[0] = 0;
   __syncthreads();
   return per;
 }
+
+// `total` units cut into `jobs` (<= total) jobs of `q` units, the first `r`
+// of them of one more.
+struct AttnCutting {
+  uint32_t total, jobs, q, r;
+  __device__ __forceinline__ uint32_t begin(uint32_t job) const { return job * q + min(job, r); }
+  __device__ __forceinline__ uint32_t job_of(uint32_t unit) const {
+    const uint32_t wide = r * (q + 1);
+    return unit < wide ? unit / (q + 1) : r + (unit - wide) / q;
+  }
+};
 
 // ------------------------------------------------------------------ one warp's part of a tile
 
@@ -177,17 +212,30 @@ constexpr int kSpare = 8;      // how far E_b may be above what the weights need
 constexpr int kMinRef = 13;    // so that 2^(127 + kBias - E_b) is finite
 constexpr int kBias = 12;      // weights enter the second product times 2^kBias: 2^(kSlack + 1 + kBias) < 2^16
 
-template <int D, int NT>
+// A tile's queries in shared memory, the same for all warps: fragments of the
+// columns (lane: column g, elements 32 b + 8 c + 0..7 of each block; FOLD = 2:
+// columns 4..7 are zero, and lane ^ 16 has the rows in columns 4..7).
+template <int D, int NT, int FOLD>
+struct __align__(16) AttnQuery {
+  uint4 frag[NT][D / 32][32];
+  float factor[8 * NT / FOLD];  // of the rows' scores
+};
+
+template <int D, int NT, int FOLD>
 struct AttnWarp {
-  static constexpr int NB = D / 32;
-  static constexpr int NJ = D / 16;
+  static constexpr int NB = D / 32, NJ = D / 16, R = 8 * NT / FOLD;
+  static constexpr int U = kStep / FOLD;  // score tiles of a step
+  using Query = AttnQuery<D, NT, FOLD>;
   float o[NT][NJ][4];          // O^T: rows d = 16 j + g (+ 8), columns 2 c (+ 1)
-  uint32_t qf[NT][NB][4];      // query fragments: column g, elements 32 b + 8 c + 0..7
-  float sc[NT][2], m[NT][2], l[NT][2];  // columns 2 c, 2 c + 1
+  float sc[NT][2], m[NT][2], l[NT][2];  // of columns 2 c, 2 c + 1
+  float limit[NT][2];          // (m + kSlack) / sc: raw scores above it move the maximum
   float unit[NB];              // 2^(127 + kBias - E_b), which tells E_b (kMinRef and up)
   uint32_t ref_half;           // E_b / 2 in bytes, with the bytes' top bits set
   int vis[NT][2];              // tokens visible to columns 2 c, 2 c + 1; INT_MAX where the column is no row
-  int vis_min, vis_max;        // over the tile's rows
+  int vis_min;                 // least of them
+
+  // Group, of the FOLD of a score tile, that this lane's columns belong to.
+  static __device__ __forceinline__ int fold() { return FOLD == 2 ? (threadIdx.x & 3) >> 1 : 0; }
 
   __device__ __forceinline__ int ref(int b) const {
     return 254 + kBias - static_cast<int>(__float_as_uint(unit[b]) >> 23);
@@ -197,50 +245,68 @@ struct AttnWarp {
     ref_half = (b == 0 ? 0x80808080u : ref_half) | static_cast<uint32_t>(min(e >> 1, 127)) << (8 * b);
   }
 
-  // Rows rho = row0 + column of the tile; sequence rows from q.lo.
-  __device__ __forceinline__ void begin(const KvAttnArgs& p, const AttnSeq& q, int64_t row0, int head) {
+  // The tile's rows, row0 on: this lane's part of column g of each tile.
+  static __device__ __forceinline__ void load_queries(const KvAttnArgs& p, const AttnSeq& q, int row0, int head,
+                                                      uint4 (&v)[NT][NB]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int64_t rows = static_cast<int64_t>(q.n) * p.group;
+    const int rows = q.n * p.group;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int64_t rho = row0 + 8 * t + g;
-      uint4 v[NB];
+      const int rho = row0 + 8 * t + g;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) v[b] = make_uint4(0, 0, 0, 0);
-      if (rho < rows) {
-        const int64_t i = rho / p.group;
-        const int64_t h = head * static_cast<int64_t>(p.group) + (rho - i * p.group);
-        const __nv_bfloat16* src = p.q + (q.lo + i) * p.q_st + h * p.q_sh + 8 * c;
+      for (int b = 0; b < NB; ++b) v[t][b] = make_uint4(0, 0, 0, 0);
+      if (8 * t + g < R && rho < rows) {
+        const int i = rho / p.group;
+        const int h = head * p.group + (rho - i * p.group);
+        const __nv_bfloat16* src = p.q + static_cast<int64_t>(q.lo + i) * p.q_st + h * p.q_sh + 8 * c;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) v[b] = *reinterpret_cast<const uint4*>(src + 32 * b);
+        for (int b = 0; b < NB; ++b) v[t][b] = *reinterpret_cast<const uint4*>(src + 32 * b);
       }
+    }
+  }
+  // The same as query fragments and score factors.
+  static __device__ __forceinline__ void put_queries(const KvAttnArgs& p, const uint4 (&v)[NT][NB], Query& to) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
       uint32_t mx = 0;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[b].x & 0x7FFF7FFFu, v[b].y & 0x7FFF7FFFu),
-                                   __vmaxu2(v[b].z & 0x7FFF7FFFu, v[b].w & 0x7FFF7FFFu)));
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[t][b].x & 0x7FFF7FFFu, v[t][b].y & 0x7FFF7FFFu),
+                                   __vmaxu2(v[t][b].z & 0x7FFF7FFFu, v[t][b].w & 0x7FFF7FFFu)));
       mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       mx = __vmaxu2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      // the row's maximum to [2^13, 2^14): exponent shift in two exact factors
+      // the row's maximum to [2^13, 2^14): exponent shift in two exact
+      // factors, with the scale's sign, so that a score's factor is not negative
       const int ex = mx == 0 ? 0 : 13 + 127 - static_cast<int>(max(mx & 0xFFFFu, mx >> 16) >> 7);
-      const float f0 = scale2(1.f, ex / 2), f1 = scale2(1.f, ex - ex / 2);
+      const float f0 = scale2(p.scale_log2 < 0.f ? -1.f : 1.f, ex / 2), f1 = scale2(1.f, ex - ex / 2);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         float f[8];
-        bf16x8_to_f32(v[b], f);
+        bf16x8_to_f32(v[t][b], f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qf[t][b][i] = pack_f16(f[2 * i] * f0 * f1, f[2 * i + 1] * f0 * f1);
+        for (int i = 0; i < 8; ++i) f[i] *= f0 * f1;
+        to.frag[t][b][lane] = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
       }
-      // 2^(e + 1 - 127) is what scores are multiplied by: one factor 2 to take back
-      const float inv = scale2(p.scale_log2, -ex - 1);
+      // key exponents count one up: one factor 2 to take back
+      if (c == 0 && 8 * t + g < R) to.factor[8 * t + g] = scale2(fabsf(p.scale_log2), -ex - 1);
+    }
+  }
+
+  __device__ __forceinline__ void begin(const KvAttnArgs& p, const AttnSeq& q, int row0, const Query& from) {
+    const int c = threadIdx.x & 3;
+    const int rows = min(q.n * p.group - row0, R);
+    const int at = row0 / p.group, off = row0 - at * p.group;
+    const int seen = q.len - q.n + at + 1;  // tokens visible to the tile's first row
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int col = 2 * c + k;
-        sc[t][k] = __shfl_sync(0xFFFFFFFFu, inv, 4 * col);
-        m[t][k] = -INFINITY;
+        const int row = (8 * t + 2 * c + k) % R;
+        sc[t][k] = from.factor[row];
+        m[t][k] = limit[t][k] = -INFINITY;
         l[t][k] = 0.f;
-        const int64_t r = row0 + 8 * t + col;
-        vis[t][k] = r < rows ? q.len - q.n + static_cast<int>(r / p.group) + 1 : INT_MAX;
+        vis[t][k] = row < rows ? seen + (off + row) / p.group : INT_MAX;
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
@@ -249,9 +315,7 @@ struct AttnWarp {
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) set_ref(b, kMinRef);
-    const int64_t last = min(row0 + 8 * NT, rows) - 1;
-    vis_min = q.len - q.n + static_cast<int>(row0 / p.group) + 1;
-    vis_max = q.len - q.n + static_cast<int>(last / p.group) + 1;
+    vis_min = seen;
   }
 
   // Code words of this lane: keys of tokens g (h = 0) and g + 8; values.
@@ -272,69 +336,90 @@ struct AttnWarp {
       vw[j] = v.x, vw[j + 1] = v.y, vw[j + 2] = v.z, vw[j + 3] = v.w;
     }
   }
-  // 2^(byte b of w - 127) as fp32 bits (0 for a byte of 0).
+  // 2^(byte b of w - 127) as fp32 (0 for a byte of 0).
   static __device__ __forceinline__ float exp_byte(uint32_t w, int b) {
     return __uint_as_float((b == 3 ? w >> 1 : w << (23 - 8 * b)) & 0x7F800000u);
   }
 
-  // S^T of one group into x (not yet scaled).
-  __device__ __forceinline__ void scores(const uint8_t* rec, float (&x)[NT][4]) {
-    const int g = (threadIdx.x & 31) >> 2;
-    uint32_t k0w[NB], k1w[NB];
-    load_keys(rec, 0, k0w);
-    load_keys(rec, 1, k1w);
-    // exponents one up (their factor 2 is in sc), so that 0 is no zero
-    const uint32_t k0 = load_exponents<NB>(rec + 16 * D + g * NB) + 0x01010101u;
-    const uint32_t k1 = load_exponents<NB>(rec + 16 * D + (g + 8) * NB) + 0x01010101u;
+  // S^T of one score tile (FOLD groups at rec) into x, not yet scaled.
+  __device__ __forceinline__ void scores(const Query& q, const uint8_t* rec, float (&x)[NT][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    uint32_t kw[FOLD][2][NB];
+#pragma unroll
+    for (int f = 0; f < FOLD; ++f)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) load_keys(rec + f * 17 * D, h, kw[f][h]);
+    // exponents of the lane's tokens, one up (the factor 2 is in sc), so that 0 is no zero
+    const uint8_t* er = rec + fold() * 17 * D + 16 * D + g * NB;
+    const uint32_t k0 = load_exponents<NB>(er) + 0x01010101u, k1 = load_exponents<NB>(er + 8 * NB) + 0x01010101u;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      uint32_t a[4], a8[4];
-      e2m1x8_to_f16(k0w[b], a);
-      e2m1x8_to_f16(k1w[b], a8);
+      float d[NT][4];
+#pragma unroll
+      for (int f = 0; f < FOLD; ++f) {
+        uint32_t a[4], a8[4];
+        e2m1x8_to_f16(kw[f][0][b], a);
+        e2m1x8_to_f16(kw[f][1][b], a8);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint4 qf = q.frag[t][b][lane ^ (16 * f)];
+          if (f == 0) mma_f16_zero(d[t], a[0], a8[0], a[1], a8[1], qf.x, qf.y);
+          else mma_f16(d[t], a[0], a8[0], a[1], a8[1], qf.x, qf.y);
+          mma_f16(d[t], a[2], a8[2], a[3], a8[3], qf.z, qf.w);
+        }
+      }
       const float f0 = exp_byte(k0, b), f1 = exp_byte(k1, b);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float d[4];
-        mma_f16_zero(d, a[0], a8[0], a[1], a8[1], qf[t][b][0], qf[t][b][1]);
-        mma_f16(d, a[2], a8[2], a[3], a8[3], qf[t][b][2], qf[t][b][3]);
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[t][k] = b == 0 ? d[k] * (k < 2 ? f0 : f1) : fmaf(d[k], k < 2 ? f0 : f1, x[t][k]);
+        for (int k = 0; k < 4; ++k)
+          x[t][k] = b == 0 ? d[t][k] * (k < 2 ? f0 : f1) : fmaf(d[t][k], k < 2 ? f0 : f1, x[t][k]);
+    }
+  }
+
+  // O^T += V_b^T (P f) for one score tile, f0 / f1 the factors of the lane's
+  // tokens g and g + 8; vw: value words of its groups.
+  __device__ __forceinline__ void value_product(const float (&pr)[NT][4], const uint32_t (&vw)[FOLD][NJ], int b,
+                                                float f0, float f1) {
+    uint32_t b0[NT], b1[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      // P^T (token g, columns 2 c, 2 c + 1) to the product's B side (column g, tokens 2 c, 2 c + 1)
+      b0[t] = movmatrix_trans(pack_f16(pr[t][0] * f0, pr[t][1] * f0));
+      b1[t] = movmatrix_trans(pack_f16(pr[t][2] * f1, pr[t][3] * f1));
+    }
+#pragma unroll
+    for (int f = 0; f < FOLD; ++f) {
+      uint32_t v0[4], v1[4];
+      e2m1x8_to_f16(vw[f][2 * b], v0);
+      e2m1x8_to_f16(vw[f][2 * b + 1], v1);
+      // columns of the other group: no weight
+      const uint32_t mine = FOLD == 1 || ((threadIdx.x >> 4) & 1) == f ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma_f16(o[t][2 * b], v0[0], v0[1], v0[2], v0[3], b0[t] & mine, b1[t] & mine);
+        mma_f16(o[t][2 * b + 1], v1[0], v1[1], v1[2], v1[3], b0[t] & mine, b1[t] & mine);
       }
     }
   }
 
-  // O^T += V_b^T (P f) for one group, f0 / f1 the factors of tokens g and g + 8.
-  __device__ __forceinline__ void value_product(const float (&pr)[NT][4], const uint32_t (&vw)[NJ], int b, float f0,
-                                                float f1) {
-    uint32_t v0[4], v1[4];
-    e2m1x8_to_f16(vw[2 * b], v0);
-    e2m1x8_to_f16(vw[2 * b + 1], v1);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      // P^T (token g, columns 2 c, 2 c + 1) to the product's B side (column g, tokens 2 c, 2 c + 1)
-      const uint32_t b0 = movmatrix_trans(pack_f16(pr[t][0] * f0, pr[t][1] * f0));
-      const uint32_t b1 = movmatrix_trans(pack_f16(pr[t][2] * f1, pr[t][3] * f1));
-      mma_f16(o[t][2 * b], v0[0], v0[1], v0[2], v0[3], b0, b1);
-      mma_f16(o[t][2 * b + 1], v1[0], v1[1], v1[2], v1[3], b0, b1);
-    }
-  }
-
-  // kStep groups at rec, rec + 17 D, from token position base on; good: bit u
-  // where group u is there (else its tokens count as unseen); len: the
-  // sequence's length.
-  __device__ __forceinline__ void step(const uint8_t* rec, uint32_t good, int base, int len) {
+  // kStep groups at rec, rec + 17 D, .., from token position base on; good:
+  // bit i where group i is there (else its tokens count as unseen); len: the
+  // sequence's length; release(): called once the records are in registers.
+  template <typename F>
+  __device__ __forceinline__ void step(const Query& q, const uint8_t* rec, uint32_t good, int base, int len, F release) {
     const int g = (threadIdx.x & 31) >> 2;
-    float x[kStep][NT][4];
-    uint32_t ve[kStep][2];
+    float x[U][NT][4];
+    uint32_t ve[U][2];
 #pragma unroll
-    for (int u = 0; u < kStep; ++u) scores(rec + u * 17 * D, x[u]);
+    for (int u = 0; u < U; ++u) scores(q, rec + u * FOLD * 17 * D, x[u]);
     // e <= E_b + 1 in every byte, compared by halves
     uint32_t fit = 0x80808080u;
 #pragma unroll
-    for (int u = 0; u < kStep; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        ve[u][h] = load_exponents<NB>(rec + u * 17 * D + 16 * D + D / 2 + (g + 8 * h) * NB);
+        ve[u][h] = load_exponents<NB>(rec + (u * FOLD + fold()) * 17 * D + 16 * D + D / 2 + (g + 8 * h) * NB);
         fit &= ref_half - ((ve[u][h] >> 1) & 0x7F7F7F7Fu);
       }
     bool slow = fit != 0x80808080u || base + kStep * kGroup > vis_min || good != (1u << kStep) - 1;
@@ -342,28 +427,26 @@ struct AttnWarp {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float mx = -INFINITY;
+        float mx = fmaxf(x[0][t][k], x[0][t][k + 2]);
 #pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-          x[u][t][k] *= sc[t][k];
-          x[u][t][k + 2] *= sc[t][k];
-          mx = fmaxf(mx, fmaxf(x[u][t][k], x[u][t][k + 2]));
-        }
-        slow |= mx > m[t][k] + kSlack;
+        for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(x[u][t][k], x[u][t][k + 2]));
+        slow |= mx > limit[t][k];
       }
     if (__any_sync(0xFFFFFFFFu, slow)) {
-      step_slow(x, rec, ve, good, base, len);
+      step_slow(x, rec, ve, good, base, len, release);
       return;
     }
 #pragma unroll
-    for (int u = 0; u < kStep; ++u) {
-      uint32_t vw[NJ];
-      load_values(rec + u * 17 * D, vw);
+    for (int u = 0; u < U; ++u) {
+      uint32_t vw[FOLD][NJ];
+#pragma unroll
+      for (int f = 0; f < FOLD; ++f) load_values(rec + (u * FOLD + f) * 17 * D, vw[f]);
+      if (u == U - 1) release();
       float pr[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) pr[t][k] = ex2(x[u][t][k] - m[t][k & 1]);
+        for (int k = 0; k < 4; ++k) pr[t][k] = ex2(fmaf(x[u][t][k], sc[t][k & 1], -m[t][k & 1]));
         l[t][0] += pr[t][0] + pr[t][2];
         l[t][1] += pr[t][1] + pr[t][3];
       }
@@ -374,33 +457,38 @@ struct AttnWarp {
   }
 
   // The same with masks, a new maximum or new references.
-  __device__ __forceinline__ void step_slow(float (&x)[kStep][NT][4], const uint8_t* rec, uint32_t (&ve)[kStep][2],
-                                            uint32_t good, int base, int len) {
+  template <typename F>
+  __device__ __forceinline__ void step_slow(float (&x)[U][NT][4], const uint8_t* rec, uint32_t (&ve)[U][2],
+                                            uint32_t good, int base, int len, F release) {
     const int g = (threadIdx.x & 31) >> 2;
     float r[NT][2];
-    int top[kStep][2];  // exponents of the largest weights of tokens g and g + 8 (p < 2^top)
-    int drop = 1000;    // how far the references may fall: the maxima's least rise
+    int top[U][2];    // exponents of the largest weights of the lane's tokens (p < 2^top)
+    int drop = 1000;  // how far the references may fall: the maxima's least rise
+    int end[U][2];    // position of the lane's tokens, INT_MAX where there is no record
 #pragma unroll
-    for (int u = 0; u < kStep; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const int gr = u * FOLD + fold();
+        const int at = (good >> gr) & 1u ? base + kGroup * gr + g + 8 * h : INT_MAX;
+        end[u][h] = at;
         top[u][h] = -1000;
-        // exponents of tokens behind the sequence may be anything: 0
-        if (base + kGroup * u + g + 8 * h >= len || !((good >> u) & 1u)) ve[u][h] = 0;
+        if (at >= len) ve[u][h] = 0;  // exponents of tokens behind the sequence may be anything
       }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const bool row = vis[t][k] != INT_MAX;
-        const int end = min(vis[t][k], len);
+        const int seen = min(vis[t][k], len);
         float mx = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kStep; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (base + kGroup * u + g + 8 * h >= end || !((good >> u) & 1u)) x[u][t][k + 2 * h] = -INFINITY;
-            mx = fmaxf(mx, x[u][t][k + 2 * h]);
+            float& y = x[u][t][k + 2 * h];
+            y = end[u][h] >= seen ? -INFINITY : y * sc[t][k];
+            mx = fmaxf(mx, y);
           }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
@@ -410,10 +498,11 @@ struct AttnWarp {
         // a column that is no row, or has met nothing yet, holds no sum that the references must keep
         if (row && m[t][k] != -INFINITY) drop = min(drop, same ? 0 : static_cast<int>(fminf(mn - m[t][k], 1000.f)));
         m[t][k] = mn;
+        limit[t][k] = sc[t][k] > 0.f ? (mn + kSlack) / sc[t][k] : (mn == -INFINITY ? -INFINITY : INFINITY);
         const float at = mn == -INFINITY ? 0.f : mn;
         l[t][k] *= r[t][k];
 #pragma unroll
-        for (int u = 0; u < kStep; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float pr = ex2(x[u][t][k + 2 * h] - at);
@@ -428,7 +517,7 @@ struct AttnWarp {
       const int old = ref(b);
       int e = max(old - drop, kMinRef), all = 0;
 #pragma unroll
-      for (int u = 0; u < kStep; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int one = static_cast<int>((ve[u][h] >> (8 * b)) & 0xFFu);
@@ -448,9 +537,11 @@ struct AttnWarp {
       }
     }
 #pragma unroll
-    for (int u = 0; u < kStep; ++u) {
-      uint32_t vw[NJ];
-      load_values(rec + u * 17 * D, vw);
+    for (int u = 0; u < U; ++u) {
+      uint32_t vw[FOLD][NJ];
+#pragma unroll
+      for (int f = 0; f < FOLD; ++f) load_values(rec + (u * FOLD + f) * 17 * D, vw[f]);
+      if (u == U - 1) release();
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int e0 = static_cast<int>((ve[u][0] >> (8 * b)) & 0xFFu) - ref(b);
@@ -465,271 +556,392 @@ struct AttnWarp {
     }
   }
 
-  // Results to shared memory: [R][kRowFloats] sums in real units, maxima and
-  // sums of weights behind them.
-  __device__ __forceinline__ void publish(float* so, float* sm, float* sl) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    constexpr int RF = AttnCfg<D, NT>::kRowFloats;
+  // Sums in real units, maxima and sums of weights of the columns; the two
+  // folds joined (then columns 2 c, 2 c + 1 of the lanes with c < 2 count).
+  __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      float own[2] = {1.f, 1.f}, other[2] = {0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[t][k] += __shfl_xor_sync(0xFFFFFFFFu, l[t][k], off);
-        if (g == 0) {
-          sm[8 * t + 2 * c + k] = m[t][k];
-          sl[8 * t + 2 * c + k] = l[t][k];
+        if constexpr (FOLD == 2) {
+          const float om = __shfl_xor_sync(0xFFFFFFFFu, m[t][k], 2), ol = __shfl_xor_sync(0xFFFFFFFFu, l[t][k], 2);
+          const float mx = fmaxf(m[t][k], om);
+          own[k] = m[t][k] == -INFINITY ? 0.f : ex2(m[t][k] - mx);
+          other[k] = om == -INFINITY ? 0.f : ex2(om - mx);
+          m[t][k] = mx;
+          l[t][k] = l[t][k] * own[k] + ol * other[k];
         }
       }
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int j = 2 * b; j < 2 * b + 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            so[(8 * t + 2 * c + (k & 1)) * RF + 16 * j + g + 8 * (k >> 1)] =
-                scale2(o[t][j][k], ref(b) - 127 - kBias);
-      }
+        for (int k = 0; k < 4; ++k) {
+          float& y = o[t][j][k];
+          y = scale2(y, ref(j / 2) - 127 - kBias);
+          if constexpr (FOLD == 2) y = y * own[k & 1] + __shfl_xor_sync(0xFFFFFFFFu, y, 2) * other[k & 1];
+        }
     }
+  }
+  // After finish(): f(row, d, value) for this lane's elements.
+  template <typename F>
+  __device__ __forceinline__ void elements(F f) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    if (FOLD == 2 && c >= 2) return;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) f(t, k & 1, 8 * t + 2 * c + (k & 1), 16 * j + g + 8 * (k >> 1), o[t][j][k]);
   }
 };
 
+// A job's part of a tile: groups [g0, g1) of sequence s and one head.
+struct AttnPiece {
+  AttnSeq q;
+  int s, head, g0, g1;
+  int row0;             // the tile's first row among the sequence's rows of a head
+  uint32_t i0, i1;      // units of the tile
+  uint32_t u, end;      // units of the piece
+  uint32_t base;        // units before sequence s
+  uint32_t job, job_u, job_end;  // the job and its units
+};
+
+// The piece that begins at unit pc.u of its job, going on from sequence pc.s.
+template <int R>
+__device__ __forceinline__ void attn_piece(const KvAttnArgs& p, AttnPiece& pc) {
+  while (pc.u >= pc.base + pc.q.tiles * pc.q.units) {
+    pc.base += pc.q.tiles * pc.q.units;
+    pc.q = attn_seq<R>(p, ++pc.s);
+  }
+  const uint32_t tile = (pc.u - pc.base) / pc.q.units;
+  pc.i0 = pc.base + tile * pc.q.units;
+  pc.i1 = pc.i0 + pc.q.units;
+  pc.end = min(pc.job_end, pc.i1);
+  const uint32_t rt = tile / p.kv.kv_heads;
+  pc.head = static_cast<int>(tile - rt * p.kv.kv_heads);
+  pc.row0 = static_cast<int>(rt * R);
+  // groups up to the last row's position
+  const int last = min(pc.row0 + R, pc.q.n * p.group) - 1;
+  const int seen = pc.q.len - pc.q.n + last / p.group + 1;
+  pc.g0 = 0;
+  pc.g1 = (max(seen, 0) + kGroup - 1) / kGroup;
+  if (p.partials != nullptr) {
+    const int from = static_cast<int>(pc.u - pc.i0) * p.unit_steps - kTileSteps;
+    const int to = static_cast<int>(pc.end - pc.i0) * p.unit_steps - kTileSteps;
+    pc.g0 = max(from, 0) * kStep;
+    pc.g1 = min(pc.g1, max(to, 0) * kStep);
+  }
+}
+
+// The first piece of a job.
+template <int R>
+__device__ __forceinline__ void attn_job(const KvAttnArgs& p, const AttnPlan& pl, int per, const AttnCutting& cut,
+                                         uint32_t job, AttnPiece& pc) {
+  pc.job = job;
+  pc.job_u = pc.u = cut.begin(job);
+  pc.job_end = cut.begin(job + 1);
+  int lo = 0, hi = min(kAttnThreads, (p.batch + per - 1) / per);  // before[lo] <= u < before[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (pl.before[mid] <= pc.u) lo = mid; else hi = mid;
+  }
+  pc.s = lo * per;
+  pc.base = pl.before[lo];
+  pc.q = attn_seq<R>(p, pc.s);
+  attn_piece<R>(p, pc);
+}
+
 // Output row `rho` of a tile's sequence and head.
 template <int D>
-__device__ __forceinline__ void attn_store(const KvAttnArgs& p, const AttnSeq& q, int64_t rho, int head, int d4,
+__device__ __forceinline__ void attn_store(const KvAttnArgs& p, int lo, int rho, int head, int d4,
                                            const float (&acc)[4], float mx, float sum) {
   const int64_t i = rho / p.group;
   const int64_t h = head * static_cast<int64_t>(p.group) + (rho - i * p.group);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
   const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
-  *reinterpret_cast<uint2*>(p.out + (q.lo + i) * p.o_st + h * p.o_sh + 4 * d4) =
+  *reinterpret_cast<uint2*>(p.out + (lo + i) * p.o_st + h * p.o_sh + 4 * d4) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   if (p.lse != nullptr && d4 == 0)
-    p.lse[(q.lo + i) * p.lse_st + h] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    p.lse[(lo + i) * p.lse_st + h] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// The rows of a tile that one warp has done alone.
+template <int D, int NT, int FOLD>
+__device__ __forceinline__ void attn_store_warp(const KvAttnArgs& p, const AttnPiece& pc, const AttnWarp<D, NT, FOLD>& w) {
+  const int rows = pc.q.n * p.group;
+  float inv[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) inv[t][k] = w.l[t][k] > 0.f ? 1.f / w.l[t][k] : 0.f;
+  w.elements([&](int t, int k, int row, int d, float v) {
+    const int rho = pc.row0 + row;
+    if (rho >= rows) return;
+    const int i = rho / p.group;
+    const int h = pc.head * p.group + (rho - i * p.group);
+    p.out[static_cast<int64_t>(pc.q.lo + i) * p.o_st + h * p.o_sh + d] = __float2bfloat16_rn(v * inv[t][k]);
+    if (p.lse != nullptr && d == 0)
+      p.lse[static_cast<int64_t>(pc.q.lo + i) * p.lse_st + h] = w.l[t][k] > 0.f ? (w.m[t][k] + log2f(w.l[t][k])) * kLn2 : -INFINITY;
+  });
 }
 
 // Weight of a partial result with maximum m under the joint maximum mx.
 __device__ __forceinline__ float join_weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
 
-// A CTA's part of a tile: groups [g0, g1) of sequence s and one head.
-struct AttnPiece {
-  AttnSeq q;
-  int s, head, g0, g1;
-  int64_t base;             // units before sequence s
-  int64_t i0, i1, u, end;   // units of the tile; of the piece
-  int64_t row0;             // the tile's first row among the sequence's rows of a head
+constexpr int kJoinThreads = 256;
+constexpr int kJoinAlone = 32;  // pieces that one warp joins alone
+
+// What a warp has of a row: the joint maximum, sum of weights, and elements
+// 4 lane .. + 3 of the sum.
+struct JoinSum {
+  float mx, sum, acc[4];
 };
 
-// The piece that begins at unit u (which [.., u1) contains), going on from
-// sequence pc.s.
-template <int R>
-__device__ __forceinline__ void attn_piece(const KvAttnArgs& p, AttnPiece& pc, int64_t u, int64_t u1) {
-  while (u >= pc.base + pc.q.tiles * pc.q.chunks) {
-    pc.base += pc.q.tiles * pc.q.chunks;
-    pc.q = attn_seq<R>(p, ++pc.s);
+// Pieces from, from + step, .. < n of a cut tile's row, several loads in flight.
+template <int D, int R>
+__device__ __forceinline__ JoinSum attn_join_pieces(const KvAttnArgs& p, const AttnCut& cut, int row, int from, int step) {
+  constexpr int L = D / 4, kAhead = 8, kPart = R * (D + 2);
+  const int lane = threadIdx.x & 31, n = cut.last - cut.first + 1;
+  // slot 1 of its job where the tile begins there, else slot 0
+  const float* part0 = p.partials + 2 * cut.first * static_cast<int64_t>(kPart);
+  JoinSum s{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+  for (int b0 = from; b0 < n; b0 += step * kAhead) {
+    float4 v[kAhead];
+    float m[kAhead], l[kAhead], top = s.mx;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int b = min(b0 + k * step, n - 1);
+      const float* pt = part0 + (2 * b + (b == 0 ? 1 : 0)) * static_cast<int64_t>(kPart);
+      m[k] = b0 + k * step < n ? pt[R * D + row] : -INFINITY;
+      l[k] = pt[R * D + R + row];
+      v[k] = reinterpret_cast<const float4*>(pt + row * D)[lane % L];
+      top = fmaxf(top, m[k]);
+    }
+    const float r = join_weight(s.mx, top);
+    s.mx = top;
+    s.sum *= r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s.acc[k] *= r;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const float f = join_weight(m[k], top);
+      s.sum = fmaf(f, l[k], s.sum);
+      s.acc[0] = fmaf(f, v[k].x, s.acc[0]);
+      s.acc[1] = fmaf(f, v[k].y, s.acc[1]);
+      s.acc[2] = fmaf(f, v[k].z, s.acc[2]);
+      s.acc[3] = fmaf(f, v[k].w, s.acc[3]);
+    }
   }
-  const int64_t tile = (u - pc.base) / pc.q.chunks;
-  pc.i0 = pc.base + tile * pc.q.chunks;
-  pc.i1 = pc.i0 + pc.q.chunks;
-  pc.u = u;
-  pc.end = min(u1, pc.i1);
-  pc.head = static_cast<int>(tile % p.kv.kv_heads);
-  pc.row0 = tile / p.kv.kv_heads * R;
-  // groups up to the last row's position
-  const int64_t last = min(pc.row0 + R, static_cast<int64_t>(pc.q.n) * p.group) - 1;
-  const int seen = pc.q.len - pc.q.n + static_cast<int>(last / p.group) + 1;
-  pc.g0 = 0;
-  pc.g1 = (max(seen, 0) + kGroup - 1) / kGroup;
-  if (p.partials != nullptr) {
-    pc.g0 = static_cast<int>(u - pc.i0) * kChunkGroups;
-    pc.g1 = min(pc.g1, static_cast<int>(pc.end - pc.i0) * kChunkGroups);
-  }
+  return s;
 }
 
-// Joins the warps' results of a piece (in shared memory) and writes the tile's
-// rows, or the piece's partial result, and then the tile if this CTA is the
-// last of its contributors.
-template <int D, int NT>
-__device__ __forceinline__ void attn_join(const KvAttnArgs& p, const AttnPiece& pc, const float* so, const float* sm,
-                                          const float* sl, int& is_last, int64_t u_begin, int64_t ctas, int64_t total) {
-  using Cfg = AttnCfg<D, NT>;
-  constexpr int R = Cfg::R, RF = Cfg::kRowFloats;
-  const bool whole = pc.u == pc.i0 && pc.end == pc.i1;
-  const int64_t rows = static_cast<int64_t>(pc.q.n) * p.group;
-  float* part = nullptr;
-  if (!whole) part = p.partials + (2 * blockIdx.x + (pc.i0 >= u_begin ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
-  for (int i = threadIdx.x; i < R * D / 4; i += kAttnThreads) {
-    const int row = i / (D / 4), d4 = i % (D / 4);
-    float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+// Rows of the cut tiles from their pieces' results, in a fixed order: a warp
+// per row, or where a tile has many pieces a CTA per row, its warps taking
+// every eighth piece.
+template <int D, int R>
+__global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const KvAttnArgs p) {
+  constexpr int W = kJoinThreads / 32, L = D / 4;
+  __shared__ float s_mx[W], s_sum[W];
+  __shared__ float4 s_acc[W][L];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_launch_dependents();
+  griddep_wait();
+  const unsigned items = p.counters->cut * R;
+  for (unsigned it = blockIdx.x * W + warp; it < items; it += gridDim.x * W) {
+    const AttnCut cut = p.cuts[it / R];
+    const int row = it % R;
+    if (row >= cut.rows || cut.last - cut.first >= kJoinAlone) continue;
+    const JoinSum s = attn_join_pieces<D, R>(p, cut, row, 0, 1);
+    if (lane < L) attn_store<D>(p, cut.lo, cut.row0 + row, cut.head, lane, s.acc, s.mx, s.sum);
+  }
+  for (unsigned it = blockIdx.x; it < items; it += gridDim.x) {
+    const AttnCut cut = p.cuts[it / R];
+    const int row = it % R;
+    if (row >= cut.rows || cut.last - cut.first < kJoinAlone) continue;
+    const JoinSum s = attn_join_pieces<D, R>(p, cut, row, warp, W);
+    if (lane < L) s_acc[warp][lane] = make_float4(s.acc[0], s.acc[1], s.acc[2], s.acc[3]);
+    if (lane == 0) {
+      s_mx[warp] = s.mx;
+      s_sum[warp] = s.sum;
+    }
+    __syncthreads();
+    if (threadIdx.x < L) {
+      float top = -INFINITY, all = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kAttnWarps; ++k) mx = fmaxf(mx, sm[k * R + row]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_mx[w]);
 #pragma unroll
-    for (int k = 0; k < kAttnWarps; ++k) {
-      const float f = join_weight(sm[k * R + row], mx);
-      const float4 v = *reinterpret_cast<const float4*>(so + (k * R + row) * RF + 4 * d4);
-      sum = fmaf(f, sl[k * R + row], sum);
-      acc[0] = fmaf(f, v.x, acc[0]);
-      acc[1] = fmaf(f, v.y, acc[1]);
-      acc[2] = fmaf(f, v.z, acc[2]);
-      acc[3] = fmaf(f, v.w, acc[3]);
-    }
-    if (whole) {
-      if (pc.row0 + row < rows) attn_store<D>(p, pc.q, pc.row0 + row, pc.head, d4, acc, mx, sum);
-    } else {
-      *reinterpret_cast<float4*>(part + row * D + 4 * d4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      if (d4 == 0) {
-        part[R * D + row] = mx;
-        part[R * D + R + row] = sum;
+      for (int w = 0; w < W; ++w) {
+        const float f = join_weight(s_mx[w], top);
+        const float4 v = s_acc[w][threadIdx.x];
+        all = fmaf(f, s_sum[w], all);
+        o[0] = fmaf(f, v.x, o[0]);
+        o[1] = fmaf(f, v.y, o[1]);
+        o[2] = fmaf(f, v.z, o[2]);
+        o[3] = fmaf(f, v.w, o[3]);
       }
+      attn_store<D>(p, cut.lo, cut.row0 + row, cut.head, threadIdx.x, o, top, all);
     }
+    __syncthreads();
   }
   __syncthreads();
-  if (whole) return;
-  // CTA that holds unit x: the largest b with b * total / ctas <= x
-  const int64_t first = ((pc.i0 + 1) * ctas - 1) / total, last = (pc.i1 * ctas - 1) / total;
-  if (threadIdx.x == 0) {
-    __threadfence();
-    const unsigned before = atomicAdd(p.counters + first, 1u);
-    is_last = before == static_cast<unsigned>(last - first);
-    if (is_last) p.counters[first] = 0;  // as found, for the next call
-    __threadfence();
-  }
-  __syncthreads();
-  if (is_last) {
-    for (int i = threadIdx.x; i < R * D / 4; i += kAttnThreads) {
-      const int row = i / (D / 4), d4 = i % (D / 4);
-      if (pc.row0 + row >= rows) continue;
-      float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int64_t b = first; b <= last; ++b) {  // slot 1: the tile begins in that CTA
-        const float* pt = p.partials + (2 * b + (b == first ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
-        mx = fmaxf(mx, __ldcg(pt + R * D + row));
-      }
-      for (int64_t b = first; b <= last; ++b) {
-        const float* pt = p.partials + (2 * b + (b == first ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
-        const float f = join_weight(__ldcg(pt + R * D + row), mx);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + row * D + 4 * d4));
-        sum = fmaf(f, __ldcg(pt + R * D + R + row), sum);
-        acc[0] = fmaf(f, v.x, acc[0]);
-        acc[1] = fmaf(f, v.y, acc[1]);
-        acc[2] = fmaf(f, v.z, acc[2]);
-        acc[3] = fmaf(f, v.w, acc[3]);
-      }
-      attn_store<D>(p, pc.q, pc.row0 + row, pc.head, d4, acc, mx, sum);
-    }
-  }
-  __syncthreads();
+  // the last CTA that has read the list leaves the counters as they were found
+  if (threadIdx.x == 0 && atomicAdd(&p.counters->done, 1u) + 1 == gridDim.x) *p.counters = AttnCounters{0, 0};
 }
 
-// A warp's ring of steps (kStep records each), filled by bulk copies that
-// its first lanes issue, one per record.
+// A warp's part of the CTA's shared memory.
+template <int D, int NT, int FOLD>
+struct __align__(128) AttnShared {
+  uint8_t ring[AttnCfg<D, NT, FOLD>::kRingBytes];
+  AttnQuery<D, NT, FOLD> query;
+  AttnPiece piece;
+  uint64_t full[kAttnStages];
+};
+
+// A warp's ring of steps (kStep records each), filled by bulk copies that its
+// lane 0 issues: one for a step whose records stand together in a page.
 template <int D>
 struct AttnRing {
-  static constexpr int S = kAttnStages, kRecord = 17 * D, kLook = 32 / kStep;
+  static constexpr int S = kAttnStages, kRecord = 17 * D;
   uint8_t* buf;
   uint64_t* bar;        // [S]
   uint32_t phase;       // bit i: parity of stage i's next completion
-  uint32_t good;        // bit kStep i + u: record u of stage i is there
-  uint64_t addr;        // lane kStep i + u: record u of the window's step i, 0 where there is none
-  int first, last;      // the piece's groups: this warp's steps begin at first, first + kChunkGroups, .. < last
+  uint32_t good;        // bits 2 i, 2 i + 1: records of stage i that are there
+  uint64_t addr;        // lane i: the first record of the window's step i; bits 0, 1: its records that are there, bit 2: together
+  int g0, steps;        // the piece's first group, and its steps
+  int last;             // behind its last group
   int issued, taken;    // steps
 
+  // The records of the 32 steps from `issued` on.
+  __device__ __forceinline__ void look(const KvCache& kv, int seq, int head) {
+    const int gi = g0 + (issued + (threadIdx.x & 31)) * kStep;
+    uint64_t a = 0, b = 0;
+    if (gi < last) a = reinterpret_cast<uint64_t>(kv_record<D>(kv, seq, gi, head));
+    if (gi + 1 < last) b = reinterpret_cast<uint64_t>(kv_record<D>(kv, seq, gi + 1, head));
+    addr = a | (a != 0 ? 1u : 0u) | (b != 0 ? 2u : 0u) | (a != 0 && b == a + kRecord ? 4u : 0u);
+  }
   __device__ __forceinline__ void issue(const KvCache& kv, int seq, int head) {
-    if (first + issued * kChunkGroups >= last) return;
-    const int lane = threadIdx.x & 31;
-    if (issued % kLook == 0) {  // look up the records of the next kLook steps
-      const int gi = first + (issued + lane / kStep) * kChunkGroups + lane % kStep;
-      addr = gi < last ? reinterpret_cast<uint64_t>(kv_record<D>(kv, seq, gi, head)) : 0;
-    }
-    const uint64_t src = __shfl_sync(0xFFFFFFFFu, addr, issued % kLook * kStep + lane % kStep);
+    if (issued >= steps) return;
+    if (issued % 32 == 0) look(kv, seq, head);
+    const uint64_t src = __shfl_sync(0xFFFFFFFFu, addr, issued % 32);
     const int st = issued % S;
-    const uint32_t there = __ballot_sync(0xFFFFFFFFu, src != 0) & ((1u << kStep) - 1);
-    good = (good & ~(((1u << kStep) - 1) << (kStep * st))) | (there << (kStep * st));
-    if (lane == 0 && there != 0) mbar_arrive_expect_tx(bar + st, __popc(there) * kRecord);
-    __syncwarp();
-    if (lane < kStep && src != 0)
-      bulk_load(buf + (st * kStep + lane) * kRecord, reinterpret_cast<const void*>(src), kRecord, bar + st);
+    const uint32_t there = static_cast<uint32_t>(src) & 3u;
+    good = (good & ~(3u << (2 * st))) | (there << (2 * st));
+    if ((threadIdx.x & 31) == 0 && there != 0) {
+      uint8_t* dst = buf + st * kStep * kRecord;
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(src & ~7ull);
+      const bool together = (src & 4u) != 0;
+      mbar_arrive_expect_tx(bar + st, there == 3u ? 2 * kRecord : kRecord);
+      if (there & 1u) bulk_load(dst, from, together ? 2 * kRecord : kRecord, bar + st);
+      if ((there & 2u) && !together)
+        bulk_load(dst + kRecord, kv_record<D>(kv, seq, g0 + issued * kStep + 1, head), kRecord, bar + st);
+    }
     ++issued;
   }
-  __device__ __forceinline__ uint32_t there(int st) const { return (good >> (kStep * st)) & ((1u << kStep) - 1); }
+  __device__ __forceinline__ uint32_t there(int st) const { return (good >> (2 * st)) & 3u; }
   __device__ __forceinline__ void begin(const KvCache& kv, const AttnPiece& pc) {
-    first = pc.g0 + (threadIdx.x >> 5) * kStep;
+    g0 = pc.g0;
     last = pc.g1;
+    steps = max(0, (pc.g1 - pc.g0 + kStep - 1) / kStep);
     issued = taken = 0;
     for (int i = 0; i < S; ++i) issue(kv, pc.s, pc.head);
   }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(const KvAttnArgs p) {
-  using Cfg = AttnCfg<D, NT>;
-  constexpr int R = Cfg::R, RF = Cfg::kRowFloats, S = kAttnStages;
+template <int D, int NT, int FOLD>
+__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kAttnCtas : 1) kv4_attn_kernel(const KvAttnArgs p) {
+  using Cfg = AttnCfg<D, NT, FOLD>;
+  constexpr int R = Cfg::R, S = kAttnStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnPlan plan;
-  __shared__ uint64_t bars[kAttnWarps][S];
-  float* so = reinterpret_cast<float*>(smem + Cfg::kRingBytes);  // [warps][R][RF]
-  float* sm = so + kAttnWarps * R * RF;                          // [warps][R]
-  float* sl = sm + kAttnWarps * R;                               // [warps][R]
-  const int warp = threadIdx.x >> 5;
-  if (threadIdx.x < kAttnWarps * S) mbar_init(&bars[0][0] + threadIdx.x, 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  AttnShared<D, NT, FOLD>& sh = reinterpret_cast<AttnShared<D, NT, FOLD>*>(smem)[warp];
+  if (lane < S) mbar_init(&sh.full[lane], 1);
   fence_mbar_init();
+  __syncwarp();
   griddep_launch_dependents();
   griddep_wait();
 
-  const int per = attn_plan<R>(p, plan);  // and makes the barriers' set-up visible to the CTA
-  const int64_t total = plan.before[kAttnThreads];
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);  // each has at least one unit
-  if (blockIdx.x >= ctas) return;
-  const int64_t u_begin = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
-  AttnPiece pc;
-  {
-    int lo = 0, hi = kAttnThreads;  // before[lo] <= u_begin < before[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (plan.before[mid] <= u_begin) lo = mid; else hi = mid;
-    }
-    pc.s = lo * per;
-    pc.base = plan.before[lo];
-    pc.q = attn_seq<R>(p, pc.s);
-  }
+  const int per = attn_plan<R>(p, plan);
+  AttnCutting cut;
+  cut.total = plan.before[kAttnThreads];
+  cut.jobs = min(gridDim.x * kAttnWarps, cut.total);
+  // a job per warp, neighbouring ones on different SMs
+  const uint32_t job = warp * gridDim.x + blockIdx.x;
+  if (job >= cut.jobs) return;
+  cut.q = cut.total / cut.jobs;
+  cut.r = cut.total - cut.q * cut.jobs;
   AttnRing<D> ring;
-  ring.buf = smem + warp * (S * kStep * Cfg::kRecord);
-  ring.bar = bars[warp];
+  ring.buf = sh.ring;
+  ring.bar = sh.full;
   ring.phase = ring.good = 0;
-  bool dead = false;  // a wait expired: no further copies or waits
-  AttnWarp<D, NT> w;
-  attn_piece<R>(p, pc, u_begin, u1);
-  ring.begin(p.kv, pc);
+  AttnWarp<D, NT, FOLD> w;
+  AttnPiece& pc = sh.piece;
+  bool dead = false;  // a wait expired
+  if (lane == 0) attn_job<R>(p, plan, per, cut, job, pc);
+  __syncwarp();
   while (true) {
-    w.begin(p, pc.q, pc.row0, pc.head);
-    for (int gi = ring.first; gi < ring.last && !dead; gi += kChunkGroups) {
+    {
+      uint4 raw[NT][D / 32];
+      w.load_queries(p, pc.q, pc.row0, pc.head, raw);
+      ring.begin(p.kv, pc);
+      w.put_queries(p, raw, sh.query);
+    }
+    __syncwarp();
+    w.begin(p, pc.q, pc.row0, sh.query);
+    const int len = pc.q.len, seq = pc.s, head = pc.head;
+    while (ring.taken < ring.steps) {
       const int st = ring.taken % S;
       const uint32_t there = ring.there(st);
-      if (there != 0) {
-        if (!warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvRecord)) {
-          dead = true;
-          break;
-        }
-        ring.phase ^= 1u << st;
-        w.step(ring.buf + st * kStep * Cfg::kRecord, there, gi * kGroup, pc.q.len);
-        __syncwarp();  // the stage is free
+      auto release = [&] {  // the stage is free
+        __syncwarp();
+        ++ring.taken;
+        ring.issue(p.kv, seq, head);
+      };
+      if (there == 0) {
+        release();
+        continue;
       }
-      ++ring.taken;
-      ring.issue(p.kv, pc.s, pc.head);
+      if (!warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvRecord)) {
+        dead = true;
+        break;
+      }
+      ring.phase ^= 1u << st;
+      w.step(sh.query, ring.buf + st * kStep * Cfg::kRecord, there, (ring.g0 + ring.taken * kStep) * kGroup, len, release);
     }
-    // the next piece's first records are on their way while this one is joined
-    const AttnPiece done = pc;
-    const bool more = pc.end < u1;
-    if (more) {
-      attn_piece<R>(p, pc, done.end, u1);
-      if (!dead) ring.begin(p.kv, pc);
+    if (dead) break;
+    // the tile's rows, or the piece's partial result
+    w.finish();
+    if (pc.u == pc.i0 && pc.end == pc.i1) {
+      attn_store_warp<D, NT, FOLD>(p, pc, w);
+    } else {
+      const bool begins = pc.i0 >= pc.job_u;
+      float* part = p.partials + (2 * pc.job + (begins ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
+      w.elements([&](int t, int k, int row, int d, float v) {
+        part[row * D + d] = v;
+        if (d == 0) {
+          part[R * D + row] = w.m[t][k];
+          part[R * D + R + row] = w.l[t][k];
+        }
+      });
+      if (begins && lane == 0)  // to the list of cut tiles
+        p.cuts[atomicAdd(&p.counters->cut, 1u)] =
+            AttnCut{static_cast<int>(pc.job), static_cast<int>(cut.job_of(pc.i1 - 1)), pc.q.lo, pc.head, pc.row0,
+                    min(pc.q.n * p.group - pc.row0, R)};
     }
-    w.publish(so + warp * R * RF, sm + warp * R, sl + warp * R);
-    __syncthreads();
-    attn_join<D, NT>(p, done, so, sm, sl, plan.last, u_begin, ctas, total);
-    if (!more) break;
+    if (pc.end >= pc.job_end) break;
+    __syncwarp();
+    if (lane == 0) {
+      pc.u = pc.end;
+      attn_piece<R>(p, pc);
+    }
+    __syncwarp();
   }
-  if (dead) {  // the copies in flight land before the CTA gives its shared memory back
+  if (dead) {  // copies in flight land before the CTA gives its shared memory back
     for (; ring.taken < ring.issued; ++ring.taken) {
       const int st = ring.taken % S;
       if (ring.there(st) != 0) warp_wait(ring.bar + st, (ring.phase >> st) & 1u, p.timeout_ns, nullptr, kSiteKvDrain);
