@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libfp8mm.so")
 SOURCES = ["fp8mm.cu", "kv4.cu"]
 HEADERS = ["ptx.cuh", "quant.cuh", "gemm.cuh", "gemm2.cuh", "decode.cuh", "kvcache.cuh", "vec.cuh", "host.cuh", "kv4.cuh",
-           "kv4_attn.cuh"]
+           "kv4_attn.cuh", "kv4_prefill.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -10,6 +10,7 @@
 
 #include "host.cuh"
 #include "kv4_attn.cuh"
+#include "kv4_prefill.cuh"
 
 namespace fp8mm {
 
@@ -79,8 +80,13 @@ static bool valid_moves(const int32_t* src, const int32_t* dst, int64_t moves, i
 // the list of cut tiles (one may begin in each job), two partial tiles per job.
 static int attn_jobs(int sms) { return kAttnCtas * kAttnWarps * sms; }
 static size_t attn_list_bytes(int sms) { return (256 + attn_jobs(sms) * sizeof(AttnCut) + 255) / 256 * 256; }
-static size_t attn_workspace(int sms, int64_t d) {  // 8 rows a tile, or 16 of half as many jobs
-  return attn_list_bytes(sms) + static_cast<size_t>(attn_jobs(sms)) * 2 * 8 * (d + 2) * sizeof(float);
+// Rows of the partial tiles: 8 per job of a warp (16 of half as many jobs), or
+// kPreRows per job of a CTA.
+static size_t attn_part_rows(int sms) {
+  return std::max(static_cast<size_t>(attn_jobs(sms)) * 2 * 8, static_cast<size_t>(sms) * 2 * kPreRows);
+}
+static size_t attn_workspace(int sms, int64_t d) {
+  return attn_list_bytes(sms) + attn_part_rows(sms) * static_cast<size_t>(d + 2) * sizeof(float);
 }
 
 template <int D, int NT, int FOLD>
@@ -94,6 +100,16 @@ static fp8mm_status launch_attn(const KvAttnArgs& p, cudaStream_t s, const Devic
   st = launch_pdl(kern, dim3(grid), dim3(kAttnThreads), smem, s, p);
   if (st != FP8MM_OK || p.partials == nullptr) return st;
   return launch_pdl(kv4_attn_join_kernel<D, Cfg::R>, dim3(2 * dev.sms), dim3(kJoinThreads), 0, s, p);
+}
+
+template <int D>
+static fp8mm_status launch_prefill(const KvAttnArgs& p, cudaStream_t s, const DeviceInfo& dev) {
+  auto kern = kv4_prefill_kernel<D>;
+  fp8mm_status st = ensure_smem(reinterpret_cast<const void*>(kern), PreCfg<D>::kSmemBytes, dev.device);
+  if (st != FP8MM_OK) return st;
+  st = launch_pdl(kern, dim3(dev.sms), dim3(kPreThreads), PreCfg<D>::kSmemBytes, s, p);
+  if (st != FP8MM_OK || p.partials == nullptr) return st;
+  return launch_pdl(kv4_attn_join_kernel<D, kPreRows>, dim3(2 * dev.sms), dim3(kJoinThreads), 0, s, p);
 }
 
 }  // namespace fp8mm
@@ -214,6 +230,7 @@ fp8mm_status mxfp4_kv_attention(const void* q_bf16, int64_t q_stride_t, int64_t 
   p.batch = static_cast<int32_t>(cache->batch);
   p.group = static_cast<int32_t>(q_heads / cache->kv_heads);
   p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = 1e-30f;  // a masked score stays -inf after scaling
   p.timeout_ns = wait_timeout_ns();
   if (workspace != nullptr) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -230,7 +247,9 @@ fp8mm_status mxfp4_kv_attention(const void* q_bf16, int64_t q_stride_t, int64_t 
   // rows that a sequence has on average decide the tile: 4, 8 or 16 of them
   const int64_t tile = cdiv(rows, cache->batch) * p.group;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 128)
+  if (p.partials != nullptr && tile >= kPreRows / 2)
+    st = d == 128 ? launch_prefill<128>(p, s, dev) : launch_prefill<64>(p, s, dev);
+  else if (d == 128)
     st = tile <= 4   ? launch_attn<128, 1, 2>(p, s, dev)
          : tile <= 8 ? launch_attn<128, 1, 1>(p, s, dev)
                      : launch_attn<128, 2, 1>(p, s, dev);

@@ -1,0 +1,601 @@
+// kv4_prefill.cuh -- attention of many query tokens per sequence over the
+// MXFP4 paged cache (chunked prefill), on tcgen05.
+//
+// The arithmetic of kv4_attn.cuh for tiles of 256 rows (query tokens x the
+// heads that share a key/value head), two halves of 128, the TMEM lanes:
+//   S = Q K^T       Q, K bf16 in shared memory, fp32 in TMEM
+//   P = 2^(S scale log2 e - m), bf16, written over S
+//   O += P V        P from TMEM, V^T bf16 in shared memory, fp32 in TMEM
+// Codes become bf16 exactly (a code has two significant bits, the exponent is
+// bf16's), so keys and values enter without error and without a range limit;
+// weights are rounded to 8 bits, and the row's sum is of the fp32 weights.  A
+// row's maximum moves only when a score passes it by 2^8, and O is scaled
+// then.
+//
+// Warps: 0-3 and 4-7 the softmax of the two halves (a thread per row), 8-11
+// bring the records and write them as bf16 tiles, 12 issues the matrix
+// instructions.  Order on the tensor pipe: PV of a half, then QK of its next
+// tile, in turns, so that one half's softmax runs beside the other's products.
+//
+// Bounds of a tile of 128 tokens (256 rows, D = 128), in SM clocks: tensor
+// 2048, exponentials 2048, shared memory 2048 (the products read 128 bytes a
+// clock of it).
+//
+// Work split: as in kv4_attn.cuh, a job per CTA in a line of costs, which here
+// follow the causal mask; cut tiles are joined by the same second kernel.
+#pragma once
+
+#include "kv4_attn.cuh"
+
+namespace fp8mm {
+
+constexpr int kPreRows = 256;        // rows of a tile
+constexpr int kPreTokens = 128;      // tokens of a step
+constexpr int kPreStages = 2;
+constexpr int kPreThreads = 416;
+constexpr int kPreConv = 4;          // warps that write key and value tiles
+constexpr float kPreSlack = 8.f;
+constexpr int kPreTileCost = 4;      // what a tile costs beside its tokens, in units of 64 tokens
+constexpr uint32_t kIdescBf16 = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kPreTokens >> 4) << 24);
+
+template <int D>
+struct PreCfg {
+  static constexpr int kBlock = 128 * 128;               // 128 rows of 64 bf16
+  static constexpr int kQBytes = kPreRows * D * 2;
+  static constexpr int kKBytes = kPreTokens * D * 2;     // D / 64 blocks of 128 rows
+  static constexpr int kVBytes = D * kPreTokens * 2;     // two blocks of D rows
+  static constexpr int kStageBytes = kKBytes + kVBytes;
+  static constexpr int kSmemBytes = kQBytes + kPreStages * kStageBytes + 1024;  // tiles stand on 1024-byte boundaries
+};
+
+// kind::f16 products, A from shared memory or from TMEM.
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+#define FP8MM_RIN32(r)                                                                                     \
+  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),       \
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),       \
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),      \
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+// 32 columns of this thread's lane, loaded and waited for in one statement, so
+// that no register is touched before it holds its value.
+__device__ __forceinline__ void tmem_load_32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : FP8MM_R32(r)
+      : "r"(taddr)
+      : "memory");
+}
+// 32 and 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::FP8MM_RIN32(r),
+      "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------------ the plan
+
+struct PreSeq {
+  int lo, n, len;
+  int rows;        // of a head
+  int tiles;       // of a head
+};
+
+__device__ __forceinline__ PreSeq pre_seq(const KvAttnArgs& p, int s) {
+  const AttnSeq q = attn_seq<kPreRows>(p, s);
+  PreSeq r;
+  r.lo = q.lo;
+  r.n = q.n;
+  r.len = q.len;
+  r.rows = q.n * p.group;
+  r.tiles = (r.rows + kPreRows - 1) / kPreRows;
+  return r;
+}
+// Cost, in units of 64 tokens, of the first `tile` row tiles of one head: a
+// tile costs its prefix and the new tokens up to its last row.
+__device__ __forceinline__ int64_t pre_cost(const KvAttnArgs& p, const PreSeq& q, int tile) {
+  const int64_t t = tile;
+  return t * (max(q.len - q.n, 0) / 64 + kPreTileCost) + t * (t + 1) / 2 * kPreRows / p.group / 64;
+}
+
+struct PrePiece {
+  PreSeq q;
+  int s, head, row0;
+  int k0, k1;              // steps of 128 tokens
+  int64_t base;            // units before sequence s
+  int64_t i0, i1, u, end;  // units of the tile; of the piece
+  int64_t job_u, job_end;
+};
+
+struct PrePlan {
+  int64_t before[kAttnThreads + 1];
+  int64_t warp_sum[kAttnThreads / 32];
+};
+
+__device__ __forceinline__ int pre_plan(const KvAttnArgs& p, PrePlan& pl) {
+  const int per = (p.batch + kAttnThreads - 1) / kAttnThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t sum = 0;
+  if (threadIdx.x < kAttnThreads) {
+    const int s1 = min(p.batch, static_cast<int>((threadIdx.x + 1) * per));
+    for (int s = threadIdx.x * per; s < s1; ++s) {
+      const PreSeq q = pre_seq(p, s);
+      sum += pre_cost(p, q, q.tiles) * p.kv.kv_heads;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) pl.warp_sum[warp] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x < kAttnThreads) {
+    for (int w = 0; w < warp; ++w) sum += pl.warp_sum[w];
+    pl.before[threadIdx.x + 1] = sum;
+    if (threadIdx.x == 0) pl.before[0] = 0;
+  }
+  __syncthreads();
+  return per;
+}
+
+// The piece that begins at unit pc.u, going on from sequence pc.s.  Within a
+// sequence the heads of a row tile stand side by side.
+__device__ __forceinline__ void pre_piece(const KvAttnArgs& p, PrePiece& pc) {
+  const int heads = p.kv.kv_heads;
+  while (pc.u >= pc.base + pre_cost(p, pc.q, pc.q.tiles) * heads) {
+    pc.base += pre_cost(p, pc.q, pc.q.tiles) * heads;
+    pc.q = pre_seq(p, ++pc.s);
+  }
+  const int64_t x = pc.u - pc.base;
+  int lo = 0, hi = pc.q.tiles;  // cost(lo) heads <= x < cost(hi) heads
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (pre_cost(p, pc.q, mid) * heads <= x) lo = mid; else hi = mid;
+  }
+  const int64_t c0 = pre_cost(p, pc.q, lo), c = pre_cost(p, pc.q, lo + 1) - c0;
+  pc.head = static_cast<int>((x - c0 * heads) / c);
+  pc.i0 = pc.base + c0 * heads + pc.head * c;
+  pc.i1 = pc.i0 + c;
+  pc.end = min(pc.job_end, pc.i1);
+  pc.row0 = lo * kPreRows;
+  const int last = min(pc.row0 + kPreRows, pc.q.rows) - 1;
+  const int seen = max(pc.q.len - pc.q.n + last / p.group + 1, 0);
+  const int64_t steps = (seen + kPreTokens - 1) / kPreTokens;
+  // the piece's share of the tile's steps
+  pc.k0 = static_cast<int>((pc.u - pc.i0) * steps / c);
+  pc.k1 = static_cast<int>((pc.end - pc.i0) * steps / c);
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D>
+struct PreShared {
+  PrePlan plan;
+  PrePiece piece;
+  uint64_t kv_full[kPreStages], kv_empty[kPreStages];
+  uint64_t s_full[2], p_full[2], pv_done[2], drain;
+  uint32_t good[kPreStages][kPreTokens / kGroup];  // whether the page table has the group
+  uint32_t tmem;
+  int abort;
+};
+
+// One group's record in registers, as the lanes of a warp hold it.
+template <int D>
+struct PreRecord {
+  static constexpr int NB = D / 32, NJ = D / 16;
+  uint32_t kw[2][NB], vw[NJ], ke[2], ve[4];  // ve: of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+  bool there;
+
+  __device__ __forceinline__ void load(const KvAttnArgs& p, int seq, int group, int groups, int head, int len) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const uint8_t* rec = group < groups ? kv_record<D>(p.kv, seq, group, head) : nullptr;
+    there = rec != nullptr || group >= groups;
+    const int base = group * kGroup;
+    if (rec != nullptr) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* kp = rec + h * 4 * D + lane * (D / 8);
+        if constexpr (NB == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(kp);
+          kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(kp);
+          kw[h][0] = v.x, kw[h][1] = v.y;
+        }
+        ke[h] = load_exponents<NB>(rec + 16 * D + (g + 8 * h) * NB);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; j += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(rec + 8 * D + (j / 4) * 512 + lane * 16);
+        vw[j] = v.x, vw[j + 1] = v.y, vw[j + 2] = v.z, vw[j + 3] = v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 2 * c + (i & 1) + 8 * (i >> 1);
+        ve[i] = load_exponents<NB>(rec + 16 * D + D / 2 + t * NB);
+        if (base + t >= len) ve[i] = 0;  // tokens behind the sequence may hold anything: finite, for weights of 0
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ke[h] = 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) kw[h][b] = 0;
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) vw[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ve[i] = 0;
+    }
+  }
+
+  // Into the bf16 tiles: keys [token][d] in blocks of 64 d, values [d][token]
+  // in blocks of 64 tokens, rows of 128 bytes whose 16-byte chunks are
+  // permuted by the row (128-byte swizzle).  at: the group's place in the tile.
+  __device__ __forceinline__ void store(uint8_t* k, uint8_t* v, int at) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int row = at * kGroup + g + 8 * h, chunk = (b & 1) * 4 + c;
+        *reinterpret_cast<uint4*>(k + (b >> 1) * PreCfg<D>::kBlock + row * 128 + ((chunk ^ g) << 4)) =
+            e2m1x8_to_bf16(kw[h][b], ue8m0_to_f32((ke[h] >> (8 * b)) & 0xFFu));
+      }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int b = j >> 1;
+      uint32_t h[4];  // (d, pair c), (d + 8, pair c), (d, pair c + 4), (d + 8, pair c + 4)
+      e2m1x8_to_f16(vw[j], h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        const float f0 = ue8m0_to_f32((ve[2 * (i >> 1)] >> (8 * b)) & 0xFFu);
+        const float f1 = ue8m0_to_f32((ve[2 * (i >> 1) + 1] >> (8 * b)) & 0xFFu);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * f0, f.y * f1);
+        const int d = 16 * j + g + 8 * (i & 1), chunk = 2 * (at & 3) + (i >> 1);
+        *reinterpret_cast<uint32_t*>(v + (at >> 2) * (D * 128) + d * 128 + ((chunk ^ g) << 4) + 4 * c) =
+            *reinterpret_cast<const uint32_t*>(&r);
+      }
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAttnArgs p) {
+  using Cfg = PreCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ PreShared<D> sh;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* qs = smem;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  volatile int* abort = &sh.abort;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPreStages; ++i) {
+      mbar_init(&sh.kv_full[i], kPreConv);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.pv_done[i], 1);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  griddep_launch_dependents();
+  griddep_wait();
+  const int per = pre_plan(p, sh.plan);
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int64_t total = sh.plan.before[kAttnThreads];
+  const int64_t jobs = min(static_cast<int64_t>(gridDim.x), total);
+  const uint64_t timeout = p.timeout_ns;
+  uint32_t tile0 = 0;  // steps of earlier pieces
+
+  if (blockIdx.x < jobs) {
+    if (threadIdx.x == 0) {
+      PrePiece& pc = sh.piece;
+      pc.job_u = pc.u = blockIdx.x * total / jobs;
+      pc.job_end = (blockIdx.x + 1) * total / jobs;
+      int lo = 0, hi = min(kAttnThreads, (p.batch + per - 1) / per);
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (sh.plan.before[mid] <= pc.u) lo = mid; else hi = mid;
+      }
+      pc.s = lo * per;
+      pc.base = sh.plan.before[lo];
+      pc.q = pre_seq(p, pc.s);
+      pre_piece(p, pc);
+    }
+    __syncthreads();
+    while (true) {
+      const PrePiece& pc = sh.piece;
+      const int row0 = pc.row0, rows = pc.q.rows, head = pc.head, len = pc.q.len, n = pc.q.n, k0 = pc.k0, k1 = pc.k1;
+      const bool whole = pc.u == pc.i0 && pc.end == pc.i1, begins = pc.i0 >= pc.job_u;
+      // queries, with the scale's sign, to shared memory
+      for (int i = threadIdx.x; i < kPreRows * D / 8; i += kPreThreads) {
+        const int r = i / (D / 8), ch = i % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row0 + r < rows) {
+          const int t = (row0 + r) / p.group, h = head * p.group + (row0 + r - t * p.group);
+          v = ld_stream_16(p.q + static_cast<int64_t>(pc.q.lo + t) * p.q_st + h * p.q_sh + 8 * ch);
+          if (p.scale_log2 < 0.f) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+        }
+        *reinterpret_cast<uint4*>(qs + (r >> 7) * (128 * D * 2) + (ch >> 3) * Cfg::kBlock + (r & 127) * 128 +
+                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      __syncthreads();
+
+      if (warp >= 8 && warp < 12) {
+        // ---- records to bf16 tiles
+        const int cw = warp - 8, groups = (len + kGroup - 1) / kGroup;
+        PreRecord<D> rec[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (k0 < k1) rec[i].load(p, pc.s, k0 * 8 + cw + 4 * i, groups, head, len);
+        for (int k = k0; k < k1; ++k) {
+          const uint32_t it = tile0 + (k - k0);
+          const int st = it % kPreStages;
+          if (!warp_wait(&sh.kv_empty[st], ((it / kPreStages) & 1) ^ 1, timeout, abort, kSiteKvRecord)) break;
+          uint8_t* ks = smem + Cfg::kQBytes + st * Cfg::kStageBytes;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            rec[i].store(ks, ks + Cfg::kKBytes, cw + 4 * i);
+            if (lane == 0) sh.good[st][cw + 4 * i] = rec[i].there;
+            if (k + 1 < k1) rec[i].load(p, pc.s, (k + 1) * 8 + cw + 4 * i, groups, head, len);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.kv_full[st]);
+        }
+      } else if (warp == 12) {
+        // ---- products
+        const uint32_t idesc_s = kIdescBf16 | (static_cast<uint32_t>(kPreTokens >> 3) << 17);
+        const uint32_t idesc_o = kIdescBf16 | (static_cast<uint32_t>(D >> 3) << 17);
+        const uint32_t q_addr = smem_u32(qs), kv_addr = smem_u32(smem + Cfg::kQBytes);
+        auto qk = [&](int t, uint32_t it) {
+          if (elect_one_sync()) {
+            const uint32_t kb = kv_addr + (it % kPreStages) * Cfg::kStageBytes;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t off = (i >> 2) * Cfg::kBlock + (i & 3) * 32;
+              mma_bf16_ss(tmem + 128 * t, sw128_kmajor_desc(q_addr + t * (128 * D * 2) + off),
+                          sw128_kmajor_desc(kb + off), idesc_s, i != 0);
+            }
+            tc_commit(&sh.s_full[t]);
+          }
+          __syncwarp();
+        };
+        bool ok = k0 >= k1 || warp_wait(&sh.kv_full[tile0 % kPreStages], (tile0 / kPreStages) & 1, timeout, abort, kSiteMmaFull);
+        if (ok && k0 < k1) {
+          tc_fence_after();
+          qk(0, tile0);
+          qk(1, tile0);
+        }
+        for (int k = k0; k < k1 && ok; ++k) {
+          const uint32_t it = tile0 + (k - k0);
+          const int st = it % kPreStages;
+          const uint32_t vb = kv_addr + st * Cfg::kStageBytes + Cfg::kKBytes;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            ok = ok && warp_wait(&sh.p_full[t], it & 1, timeout, abort, kSiteMmaAccEmpty);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one_sync()) {
+#pragma unroll
+              for (int i = 0; i < kPreTokens / 16; ++i)
+                mma_bf16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i,
+                            sw128_kmajor_desc(vb + (i >> 2) * (D * 128) + (i & 3) * 32), idesc_o, k != k0 || i != 0);
+              tc_commit(&sh.pv_done[t]);
+              if (t == 1) tc_commit(&sh.kv_empty[st]);
+            }
+            __syncwarp();
+            if (k + 1 < k1) {
+              if (t == 0) {
+                ok = warp_wait(&sh.kv_full[(it + 1) % kPreStages], ((it + 1) / kPreStages) & 1, timeout, abort, kSiteMmaFull);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              qk(t, it + 1);
+            }
+          }
+        }
+      } else {
+        // ---- softmax: a thread per row
+        const int t = warp >> 2, r = threadIdx.x & 127;
+        const int rho = row0 + 128 * t + r;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + 128 * t + lane_base, o_addr = tmem + 256 + 128 * t + lane_base;
+        const int vis = rho < rows ? min(len, max(len - n + rho / p.group + 1, 0)) : 0;
+        const float sc = fabsf(p.scale_log2);
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int k = k0; k < k1; ++k) {
+          const uint32_t it = tile0 + (k - k0);
+          ok = warp_wait(&sh.s_full[t], it & 1, timeout, abort, kSiteEpiAccFull);
+          if (!ok) break;
+          tc_fence_after();
+          // groups that the page table does not have count as unseen
+          uint32_t all = 1;
+#pragma unroll
+          for (int i = 0; i < kPreTokens / kGroup; ++i) all &= sh.good[it % kPreStages][i];
+          const int base = k * kPreTokens;
+          const bool masked = __any_sync(0xFFFFFFFFu, base + kPreTokens > vis) || !all;
+          // 32 scores at a time: read once for the maximum, once for the weights
+          auto mask = [&](uint32_t (&s)[32], int i) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (base + 32 * i + e >= vis || (!all && !sh.good[it % kPreStages][2 * i + e / kGroup])) s[e] = 0xFF800000u;
+          };
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t s[32];
+            tmem_load_32(s_addr + 32 * i, s);
+            if (masked) mask(s, i);
+            float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
+#pragma unroll
+            for (int e = 2; e < 32; e += 2) {
+              a = fmaxf(a, __uint_as_float(s[e]));
+              b = fmaxf(b, __uint_as_float(s[e + 1]));
+            }
+            mx = fmaxf(mx, fmaxf(a, b));
+          }
+          mx *= sc;
+          float f = 1.f;
+          if (mx > m + kPreSlack || (m == -INFINITY && mx != -INFINITY)) {
+            f = ex2(m - mx);
+            m = mx;
+            l *= f;
+          }
+          if (__any_sync(0xFFFFFFFFu, f != 1.f) && k != k0) {
+            // scale what is summed; the products of the step before have landed first
+            ok = warp_wait(&sh.pv_done[t], (it & 1) ^ 1, timeout, abort, kSiteEpiSync);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[32];
+              tmem_load_32(o_addr + 32 * i, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x32(o_addr + 32 * i, o);
+            }
+            tmem_st_wait();
+          }
+          const float at = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // weights of 32 scores take 16 columns, of scores that have been read
+            uint32_t s[32];
+            tmem_load_32(s_addr + 32 * i, s);
+            if (masked) mask(s, i);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float a = ex2(fmaf(__uint_as_float(s[2 * e]), sc, -at));
+              const float b = ex2(fmaf(__uint_as_float(s[2 * e + 1]), sc, -at));
+              sum[e & 1] += a;
+              sum[2 + (e & 1)] += b;
+              const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+              w[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            tmem_st_32x32b_x16(s_addr + 16 * i, w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[t]);
+        }
+        // ---- the rows, or the piece's partial result
+        const uint32_t last = tile0 + (k1 - k0) - 1;
+        if (ok && k0 < k1) ok = warp_wait(&sh.pv_done[t], last & 1, timeout, abort, kSiteEpiSync);
+        if (ok) {
+          tc_fence_after();
+          const bool row = rho < rows;
+          float* part = nullptr;
+          __nv_bfloat16* out = nullptr;
+          const int tok = rho / p.group, h = head * p.group + (rho - tok * p.group);
+          if (!whole) part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * (kPreRows * (D + 2));
+          else out = p.out + static_cast<int64_t>(pc.q.lo + tok) * p.o_st + h * p.o_sh;
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            if (k0 < k1) {
+              tmem_load_32(o_addr + 32 * i, o);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0;
+            }
+            if (!whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4*>(part + (128 * t + r) * D + 32 * i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            } else if (row) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * j]) * inv, __uint_as_float(o[e + 2 * j + 1]) * inv);
+                  w[j] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                *reinterpret_cast<uint4*>(out + 32 * i + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+          if (!whole) {
+            part[kPreRows * D + 128 * t + r] = m;
+            part[kPreRows * D + kPreRows + 128 * t + r] = l;
+          } else if (row && p.lse != nullptr) {
+            p.lse[static_cast<int64_t>(pc.q.lo + tok) * p.lse_st + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          }
+          tc_fence_before();
+        }
+      }
+      if (!whole && begins && threadIdx.x == 0) {  // to the list of cut tiles
+        const int64_t last = (pc.i1 * jobs - 1) / total;  // the job that holds unit i1 - 1
+        p.cuts[atomicAdd(&p.counters->cut, 1u)] =
+            AttnCut{static_cast<int>(blockIdx.x), static_cast<int>(last), pc.q.lo, head, row0, min(rows - row0, kPreRows)};
+      }
+      tile0 += k1 - k0;
+      __syncthreads();
+      tc_fence_after();
+      if (pc.end >= pc.job_end || *abort != 0) break;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        sh.piece.u = sh.piece.end;
+        pre_piece(p, sh.piece);
+      }
+      __syncthreads();
+    }
+  }
+  // the matrix instructions in flight land before the tensor memory is given back
+  if (warp == 12) {
+    if (elect_one_sync()) tc_commit(&sh.drain);
+    __syncwarp();
+    warp_wait(&sh.drain, 0, timeout, nullptr, kSiteDrain);
+  }
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace fp8mm

@@ -72,7 +72,12 @@ def _filled(rng, lengths, page_size, heads, dim, seed, make=_kv):
     return cache, table, own
 
 
-def _check_attention(out, lse, q, cache, own, lengths, cu, scale):
+# rows of a head per sequence, on average, from which the tcgen05 kernel runs (with a workspace); it rounds weights to
+# bf16 (2^-8 of each) where the other rounds them to f16
+MANY_ROWS, BF16_WEIGHTS = 128, 2.0 ** -8 + 2.0 ** -11
+
+
+def _check_attention(out, lse, q, cache, own, lengths, cu, scale, weights=2.0 ** -10):
     out, lse = out.double().cpu(), None if lse is None else lse.double().cpu()
     for s, length in enumerate(lengths):
         rows = slice(cu[s], cu[s + 1])
@@ -80,7 +85,7 @@ def _check_attention(out, lse, q, cache, own, lengths, cu, scale):
         want, mag, wlse = ref.attention(q[rows], k, v, scale)
         top = v.abs().amax(0).unflatten(-1, (-1, 32)).amax(-1).repeat_interleave(32, -1) if length else torch.zeros(cache.heads, cache.dim)
         top = top.repeat_interleave(q.shape[1] // cache.heads, 0)
-        lim = 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag + length * 2.0 ** -31 * top + 1e-37
+        lim = 2.0 ** -8 * want.abs() + weights * mag + length * 2.0 ** -31 * top + 1e-37
         bad = (out[rows] - want).abs() / lim
         assert torch.isfinite(out[rows]).all() and (bad.numel() == 0 or bad.max() <= 1), (s, bad.max(), bad.argmax(), want.flatten()[bad.argmax()], out[rows].flatten()[bad.argmax()], lim.flatten()[bad.argmax()])
         if lse is not None:
@@ -227,8 +232,32 @@ def test_several_queries_are_causal(dim, q_heads, kv_heads, new, lengths):
         lse = torch.full((rows, q_heads), 5.0, device="cuda")
         fp8mm.mxfp4_kv_attention(qd, cache.data.cuda(), _i32(table), _i32(lengths), 32, cu_seqlens=_i32(cu), scale=0.2,
                                  out=out, lse=lse, workspace=workspace)
-        _check_attention(out, lse, q, cache, own, lengths, cu, 0.2)
+        many = workspace is not None and -(-rows // len(new)) * (q_heads // kv_heads) >= MANY_ROWS
+        _check_attention(out, lse, q, cache, own, lengths, cu, 0.2, BF16_WEIGHTS if many else 2.0 ** -10)
         assert (out[cu[-1]:] == 5).all() and (lse[cu[-1]:] == 5).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_heads,kv_heads", [(8, 2), (3, 3), (5, 1), (16, 1)])
+@pytest.mark.parametrize("new,lengths", [([300], [300]), ([257, 1, 0, 130], [600, 400, 50, 100]), ([129, 128], [127, 1100])])
+def test_chunks_of_prompts(dim, q_heads, kv_heads, new, lengths):
+    """Many queries a sequence: no prefix, long prefixes, a sequence shorter than its queries, empty and single ones."""
+    rng = np.random.default_rng(9)
+    cache, table, own = _filled(rng, lengths, 64, kv_heads, dim, 61)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = torch.randn(cu[-1] + 1, q_heads, dim, generator=torch.Generator().manual_seed(4)).bfloat16()
+    ws = torch.zeros(fp8mm.mxfp4_kv_attention_workspace_bytes(dim), dtype=torch.uint8, device="cuda")
+    for scale in (dim ** -0.5, -0.3):
+        out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full(q.shape[:2], 5.0, device="cuda")
+        for _ in range(2):                                 # twice on one workspace: the same bits
+            before = out.clone()
+            fp8mm.mxfp4_kv_attention(q.cuda(), cache.data.cuda(), _i32(table), _i32(lengths), 64, cu_seqlens=_i32(cu),
+                                     scale=scale, out=out, lse=lse, workspace=ws)
+        assert torch.equal(before, out)
+        _check_attention(out, lse, q, cache, own, lengths, cu, scale, BF16_WEIGHTS)
+        assert (out[cu[-1]:] == 5).all() and (lse[cu[-1]:] == 5).all()
+    assert not ws.view(torch.int32)[:64].any()
 
 
 def _uneven(n, heads, dim, seed):
@@ -254,6 +283,11 @@ def test_uneven_magnitudes(dim, sharp):
     q[:, 1] = (q[:, 1].double() * 2.0 ** -40).bfloat16()
     out = fp8mm.mxfp4_kv_attention(q.cuda(), cache.data.cuda(), _i32(table), _i32(lengths), 64, scale=sharp)
     _check_attention(out, None, q, cache, own, lengths, range(3), sharp)
+    q = q.repeat_interleave(40, 0)                         # 40 queries a sequence, on the kernel for many
+    ws = torch.zeros(fp8mm.mxfp4_kv_attention_workspace_bytes(dim), dtype=torch.uint8, device="cuda")
+    out = fp8mm.mxfp4_kv_attention(q.cuda(), cache.data.cuda(), _i32(table), _i32(lengths), 64, cu_seqlens=_i32([0, 40, 80]),
+                                   scale=sharp, workspace=ws)
+    _check_attention(out, None, q, cache, own, lengths, [0, 40, 80], sharp, BF16_WEIGHTS)
 
 
 def test_outlier_value_with_no_weight():
