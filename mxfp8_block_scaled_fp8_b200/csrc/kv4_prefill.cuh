@@ -4,7 +4,7 @@
 // The arithmetic of kv4_attn.cuh for tiles of 256 rows (query tokens x the
 // heads that share a key/value head), two halves of 128, the TMEM lanes:
 //   S = Q K^T       Q, K bf16 in shared memory, fp32 in TMEM
-//   P = 2^(S scale log2 e - m), bf16, written over S
+//   P = 2^(S scale log2 e - m), bf16, written over the second half of S
 //   O += P V        P from TMEM, V^T bf16 in shared memory, fp32 in TMEM
 // Codes become bf16 exactly (a code has two significant bits, the exponent is
 // bf16's), so keys and values enter without error and without a range limit;
@@ -12,9 +12,9 @@
 // row's maximum moves only when a score passes it by 2^8, and O is scaled
 // then.
 //
-// Warps: 0-3 and 4-7 the softmax of the two halves (a thread per row), 8-11
-// bring the records and write them as bf16 tiles, 12 issues the matrix
-// instructions.  Order on the tensor pipe: PV of a half, then QK of its next
+// Warps: 0-3 and 4-7 the softmax of the two halves (a thread per row), 8-10
+// bring keys and 11-14 values and write them as bf16 tiles, 15 issues the
+// matrix instructions.  Order on the tensor pipe: PV of a half, then QK of its next
 // tile, in turns, so that one half's softmax runs beside the other's products.
 //
 // Bounds of a tile of 128 tokens (256 rows, D = 128), in SM clocks: tensor
@@ -32,8 +32,8 @@ namespace fp8mm {
 constexpr int kPreRows = 256;        // rows of a tile
 constexpr int kPreTokens = 128;      // tokens of a step
 constexpr int kPreStages = 2;
-constexpr int kPreThreads = 416;
-constexpr int kPreConv = 4;          // warps that write key and value tiles
+constexpr int kPreThreads = 512;
+constexpr int kPreKeyWarps = 3, kPreValueWarps = 4;  // that write key and value tiles: 8 groups of a step each
 constexpr float kPreSlack = 8.f;
 constexpr int kPreTileCost = 4;      // what a tile costs beside its tokens, in units of 64 tokens
 constexpr uint32_t kIdescBf16 = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kPreTokens >> 4) << 24);
@@ -79,6 +79,25 @@ __device__ __forceinline__ void tmem_load_32(uint32_t taddr, uint32_t (&r)[32]) 
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : FP8MM_R32(r)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load_64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
 }
@@ -202,92 +221,121 @@ struct PreShared {
   PrePiece piece;
   uint64_t kv_full[kPreStages], kv_empty[kPreStages];
   uint64_t s_full[2], p_full[2], pv_done[2], drain;
-  uint32_t good[kPreStages][kPreTokens / kGroup];  // whether the page table has the group
   uint32_t tmem;
   int abort;
 };
 
-// One group's record in registers, as the lanes of a warp hold it.
+// One group's keys or values in registers, as the lanes of a warp hold them
+// (zeros without a record); base: position of its first token.
 template <int D>
-struct PreRecord {
-  static constexpr int NB = D / 32, NJ = D / 16;
-  uint32_t kw[2][NB], vw[NJ], ke[2], ve[4];  // ve: of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-  bool there;
+struct PreKeys {
+  static constexpr int NB = D / 32;
+  uint32_t w[2][NB], e[2];
 
-  __device__ __forceinline__ void load(const KvAttnArgs& p, int seq, int group, int groups, int head, int len) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint8_t* rec = group < groups ? kv_record<D>(p.kv, seq, group, head) : nullptr;
-    there = rec != nullptr || group >= groups;
-    const int base = group * kGroup;
-    if (rec != nullptr) {
+  __device__ __forceinline__ void load(const uint8_t* rec, int, int) {
+    const int lane = threadIdx.x & 31, g = lane >> 2;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* kp = rec + h * 4 * D + lane * (D / 8);
-        if constexpr (NB == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(kp);
-          kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(kp);
-          kw[h][0] = v.x, kw[h][1] = v.y;
-        }
-        ke[h] = load_exponents<NB>(rec + 16 * D + (g + 8 * h) * NB);
+    for (int h = 0; h < 2; ++h) {
+      e[h] = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) w[h][b] = 0;
+      if (rec == nullptr) continue;
+      const uint8_t* kp = rec + h * 4 * D + lane * (D / 8);
+      if constexpr (NB == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(kp);
+        w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(kp);
+        w[h][0] = v.x, w[h][1] = v.y;
       }
-#pragma unroll
-      for (int j = 0; j < NJ; j += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(rec + 8 * D + (j / 4) * 512 + lane * 16);
-        vw[j] = v.x, vw[j + 1] = v.y, vw[j + 2] = v.z, vw[j + 3] = v.w;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 2 * c + (i & 1) + 8 * (i >> 1);
-        ve[i] = load_exponents<NB>(rec + 16 * D + D / 2 + t * NB);
-        if (base + t >= len) ve[i] = 0;  // tokens behind the sequence may hold anything: finite, for weights of 0
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ke[h] = 0;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) kw[h][b] = 0;
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) vw[j] = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ve[i] = 0;
+      e[h] = load_exponents<NB>(rec + 16 * D + (g + 8 * h) * NB);
     }
   }
-
-  // Into the bf16 tiles: keys [token][d] in blocks of 64 d, values [d][token]
-  // in blocks of 64 tokens, rows of 128 bytes whose 16-byte chunks are
-  // permuted by the row (128-byte swizzle).  at: the group's place in the tile.
-  __device__ __forceinline__ void store(uint8_t* k, uint8_t* v, int at) const {
+  // Into the tile [token][d]: blocks of 64 d, rows of 128 bytes whose 16-byte
+  // chunks are permuted by the row (128-byte swizzle).  at: the group's place.
+  __device__ __forceinline__ void store(uint8_t* tile, int at) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int row = at * kGroup + g + 8 * h, chunk = (b & 1) * 4 + c;
-        *reinterpret_cast<uint4*>(k + (b >> 1) * PreCfg<D>::kBlock + row * 128 + ((chunk ^ g) << 4)) =
-            e2m1x8_to_bf16(kw[h][b], ue8m0_to_f32((ke[h] >> (8 * b)) & 0xFFu));
+        *reinterpret_cast<uint4*>(tile + (b >> 1) * PreCfg<D>::kBlock + row * 128 + ((chunk ^ g) << 4)) =
+            e2m1x8_to_bf16(w[h][b], ue8m0_to_f32((e[h] >> (8 * b)) & 0xFFu));
       }
+  }
+};
+
+template <int D>
+struct PreValues {
+  static constexpr int NB = D / 32, NJ = D / 16;
+  uint32_t w[NJ], e[4];  // e: of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+
+  __device__ __forceinline__ void load(const uint8_t* rec, int base, int len) {
+    const int lane = threadIdx.x & 31, c = lane & 3;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int b = j >> 1;
-      uint32_t h[4];  // (d, pair c), (d + 8, pair c), (d, pair c + 4), (d + 8, pair c + 4)
-      e2m1x8_to_f16(vw[j], h);
+    for (int j = 0; j < NJ; ++j) w[j] = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        const float f0 = ue8m0_to_f32((ve[2 * (i >> 1)] >> (8 * b)) & 0xFFu);
-        const float f1 = ue8m0_to_f32((ve[2 * (i >> 1) + 1] >> (8 * b)) & 0xFFu);
-        const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * f0, f.y * f1);
-        const int d = 16 * j + g + 8 * (i & 1), chunk = 2 * (at & 3) + (i >> 1);
-        *reinterpret_cast<uint32_t*>(v + (at >> 2) * (D * 128) + d * 128 + ((chunk ^ g) << 4) + 4 * c) =
-            *reinterpret_cast<const uint32_t*>(&r);
+    for (int i = 0; i < 4; ++i) e[i] = 0;
+    if (rec == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < NJ; j += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(rec + 8 * D + (j / 4) * 512 + lane * 16);
+      w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 2 * c + (i & 1) + 8 * (i >> 1);
+      // tokens behind the sequence may hold anything: exponent 0, finite, for weights of 0
+      if (base + t < len) e[i] = load_exponents<NB>(rec + 16 * D + D / 2 + t * NB);
+    }
+  }
+  // Into the tile [d][token]: blocks of 64 tokens, swizzled rows as the keys'.
+  __device__ __forceinline__ void store(uint8_t* tile, int at) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = ue8m0_to_f32((e[i] >> (8 * b)) & 0xFFu);
+#pragma unroll
+      for (int j = 2 * b; j < 2 * b + 2; ++j) {
+        uint32_t h[4];  // (d, pair c), (d + 8, pair c), (d, pair c + 4), (d + 8, pair c + 4)
+        e2m1x8_to_f16(w[j], h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+          const __nv_bfloat162 r = __floats2bfloat162_rn(v.x * f[2 * (i >> 1)], v.y * f[2 * (i >> 1) + 1]);
+          const int d = 16 * j + g + 8 * (i & 1), chunk = 2 * (at & 3) + (i >> 1);
+          *reinterpret_cast<uint32_t*>(tile + (at >> 2) * (D * 128) + d * 128 + ((chunk ^ g) << 4) + 4 * c) =
+              *reinterpret_cast<const uint32_t*>(&r);
+        }
       }
     }
   }
 };
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAttnArgs p) {
@@ -300,7 +348,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
   volatile int* abort = &sh.abort;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPreStages; ++i) {
-      mbar_init(&sh.kv_full[i], kPreConv);
+      mbar_init(&sh.kv_full[i], kPreKeyWarps + kPreValueWarps);
       mbar_init(&sh.kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -312,7 +360,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 15) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
@@ -325,6 +373,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
   const int64_t total = sh.plan.before[kAttnThreads];
   const int64_t jobs = min(static_cast<int64_t>(gridDim.x), total);
   const uint64_t timeout = p.timeout_ns;
+  // registers: 512 threads at 128 become 256 at 160 (softmax) and 256 at 96
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   uint32_t tile0 = 0;  // steps of earlier pieces
 
   if (blockIdx.x < jobs) {
@@ -348,43 +399,68 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
       const int row0 = pc.row0, rows = pc.q.rows, head = pc.head, len = pc.q.len, n = pc.q.n, k0 = pc.k0, k1 = pc.k1;
       const bool whole = pc.u == pc.i0 && pc.end == pc.i1, begins = pc.i0 >= pc.job_u;
       // queries, with the scale's sign, to shared memory
-      for (int i = threadIdx.x; i < kPreRows * D / 8; i += kPreThreads) {
-        const int r = i / (D / 8), ch = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row0 + r < rows) {
-          const int t = (row0 + r) / p.group, h = head * p.group + (row0 + r - t * p.group);
-          v = ld_stream_16(p.q + static_cast<int64_t>(pc.q.lo + t) * p.q_st + h * p.q_sh + 8 * ch);
-          if (p.scale_log2 < 0.f) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+      {
+        constexpr int N = kPreRows * D / 8 / kPreThreads;
+        uint4 v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int i = threadIdx.x + j * kPreThreads, r = i / (D / 8), ch = i % (D / 8);
+          v[j] = make_uint4(0, 0, 0, 0);
+          if (row0 + r < rows) {
+            const int t = (row0 + r) / p.group, h = head * p.group + (row0 + r - t * p.group);
+            v[j] = ld_stream_16(p.q + static_cast<int64_t>(pc.q.lo + t) * p.q_st + h * p.q_sh + 8 * ch);
+          }
         }
-        *reinterpret_cast<uint4*>(qs + (r >> 7) * (128 * D * 2) + (ch >> 3) * Cfg::kBlock + (r & 127) * 128 +
-                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
+        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int i = threadIdx.x + j * kPreThreads, r = i / (D / 8), ch = i % (D / 8);
+          *reinterpret_cast<uint4*>(qs + (r >> 7) * (128 * D * 2) + (ch >> 3) * Cfg::kBlock + (r & 127) * 128 +
+                                    (((ch & 7) ^ (r & 7)) << 4)) =
+              make_uint4(v[j].x ^ sign, v[j].y ^ sign, v[j].z ^ sign, v[j].w ^ sign);
+        }
       }
       fence_proxy_async_smem();
       __syncthreads();
 
-      if (warp >= 8 && warp < 12) {
-        // ---- records to bf16 tiles
-        const int cw = warp - 8, groups = (len + kGroup - 1) / kGroup;
-        PreRecord<D> rec[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (k0 < k1) rec[i].load(p, pc.s, k0 * 8 + cw + 4 * i, groups, head, len);
-        for (int k = k0; k < k1; ++k) {
-          const uint32_t it = tile0 + (k - k0);
-          const int st = it % kPreStages;
-          if (!warp_wait(&sh.kv_empty[st], ((it / kPreStages) & 1) ^ 1, timeout, abort, kSiteKvRecord)) break;
-          uint8_t* ks = smem + Cfg::kQBytes + st * Cfg::kStageBytes;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            rec[i].store(ks, ks + Cfg::kKBytes, cw + 4 * i);
-            if (lane == 0) sh.good[st][cw + 4 * i] = rec[i].there;
-            if (k + 1 < k1) rec[i].load(p, pc.s, (k + 1) * 8 + cw + 4 * i, groups, head, len);
+      if (warp >= 8 && warp < 15) {
+        // ---- records to bf16 tiles, a step ahead in registers
+        const int groups = (len + kGroup - 1) / kGroup, seq = pc.s;
+        // this warp's groups of a step: first, first + warps, .. < 8; one is
+        // written while the next is on its way
+        auto bring = [&](auto rec, int first, int warps, int offset) {
+          const int per = (8 - first + warps - 1) / warps, units = (k1 - k0) * per;
+          uint64_t addr = 0;  // lane i: the record of unit 32 n + i
+          auto load = [&](int unit) {
+            if ((unit & 31) == 0) {
+              const int u = unit + lane, group = (k0 + u / per) * 8 + first + u % per * warps;
+              addr = u < units && group < groups ? reinterpret_cast<uint64_t>(kv_record<D>(p.kv, seq, group, head)) : 0;
+            }
+            const uint64_t a = __shfl_sync(0xFFFFFFFFu, addr, unit & 31);
+            rec.load(reinterpret_cast<const uint8_t*>(a), ((k0 + unit / per) * 8 + first + unit % per * warps) * kGroup, len);
+          };
+          if (units > 0) load(0);
+#pragma unroll 1
+          for (int unit = 0; unit < units; ++unit) {
+            const int step = unit / per, i = unit - step * per;
+            const uint32_t it = tile0 + step;
+            const int st = it % kPreStages;
+            auto cur = rec;
+            if (unit + 1 < units) load(unit + 1);
+            if (i == 0 && !warp_wait(&sh.kv_empty[st], ((it / kPreStages) & 1) ^ 1, timeout, abort, kSiteKvRecord)) break;
+            cur.store(smem + Cfg::kQBytes + st * Cfg::kStageBytes + offset, first + i * warps);
+            if (i == per - 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.kv_full[st]);
+            }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.kv_full[st]);
-        }
-      } else if (warp == 12) {
+        };
+        if (warp < 8 + kPreKeyWarps)
+          bring(PreKeys<D>(), warp - 8, kPreKeyWarps, 0);
+        else
+          bring(PreValues<D>(), warp - 8 - kPreKeyWarps, kPreValueWarps, Cfg::kKBytes);
+      } else if (warp == 15) {
         // ---- products
         const uint32_t idesc_s = kIdescBf16 | (static_cast<uint32_t>(kPreTokens >> 3) << 17);
         const uint32_t idesc_o = kIdescBf16 | (static_cast<uint32_t>(D >> 3) << 17);
@@ -420,7 +496,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
             if (elect_one_sync()) {
 #pragma unroll
               for (int i = 0; i < kPreTokens / 16; ++i)
-                mma_bf16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i,
+                mma_bf16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 64 + 8 * i,
                             sw128_kmajor_desc(vb + (i >> 2) * (D * 128) + (i & 3) * 32), idesc_o, k != k0 || i != 0);
               tc_commit(&sh.pv_done[t]);
               if (t == 1) tc_commit(&sh.kv_empty[st]);
@@ -451,32 +527,31 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           ok = warp_wait(&sh.s_full[t], it & 1, timeout, abort, kSiteEpiAccFull);
           if (!ok) break;
           tc_fence_after();
-          // groups that the page table does not have count as unseen
-          uint32_t all = 1;
+          const int left = vis - k * kPreTokens;  // tokens of the step that the row sees
+          const bool masked = __any_sync(0xFFFFFFFFu, left < kPreTokens);
+          auto mask = [](uint32_t (&s)[64], int left) {
 #pragma unroll
-          for (int i = 0; i < kPreTokens / kGroup; ++i) all &= sh.good[it % kPreStages][i];
-          const int base = k * kPreTokens;
-          const bool masked = __any_sync(0xFFFFFFFFu, base + kPreTokens > vis) || !all;
-          // 32 scores at a time: read once for the maximum, once for the weights
-          auto mask = [&](uint32_t (&s)[32], int i) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (base + 32 * i + e >= vis || (!all && !sh.good[it % kPreStages][2 * i + e / kGroup])) s[e] = 0xFF800000u;
+            for (int e = 0; e < 64; ++e)
+              if (e >= left) s[e] = 0xFF800000u;
           };
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t s[32];
-            tmem_load_32(s_addr + 32 * i, s);
-            if (masked) mask(s, i);
+          auto top = [](const uint32_t (&s)[64]) {
             float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
 #pragma unroll
-            for (int e = 2; e < 32; e += 2) {
+            for (int e = 2; e < 64; e += 2) {
               a = fmaxf(a, __uint_as_float(s[e]));
               b = fmaxf(b, __uint_as_float(s[e + 1]));
             }
-            mx = fmaxf(mx, fmaxf(a, b));
-          }
+            return fmaxf(a, b);
+          };
+          // the first half of the scores is read twice (for the maximum, for
+          // the weights), the second half stays in registers
+          uint32_t s[64];
+          tmem_load_64(s_addr, s);
+          if (masked) mask(s, left);
+          float mx = top(s);
+          tmem_load_64(s_addr + 64, s);
+          if (masked) mask(s, left - 64);
+          mx = fmaxf(mx, top(s));
           mx *= sc;
           float f = 1.f;
           if (mx > m + kPreSlack || (m == -INFINITY && mx != -INFINITY)) {
@@ -489,7 +564,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
             ok = warp_wait(&sh.pv_done[t], (it & 1) ^ 1, timeout, abort, kSiteEpiSync);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
               uint32_t o[32];
               tmem_load_32(o_addr + 32 * i, o);
@@ -500,25 +575,32 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
             tmem_st_wait();
           }
           const float at = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sc2 = pack2(sc, sc), at2 = pack2(-at, -at);
+          uint64_t sum[2] = {0, 0};
+          // 64 weights of s to 32 columns; the place is free: S's second half has been read
+          auto weights = [&](const uint32_t (&s)[64], int half) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // weights of 32 scores take 16 columns, of scores that have been read
-            uint32_t s[32];
-            tmem_load_32(s_addr + 32 * i, s);
-            if (masked) mask(s, i);
-            uint32_t w[16];
+            for (int q = 0; q < 2; ++q) {
+              uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float a = ex2(fmaf(__uint_as_float(s[2 * e]), sc, -at));
-              const float b = ex2(fmaf(__uint_as_float(s[2 * e + 1]), sc, -at));
-              sum[e & 1] += a;
-              sum[2 + (e & 1)] += b;
-              const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-              w[e] = *reinterpret_cast<const uint32_t*>(&v);
+              for (int e = 0; e < 16; ++e) {
+                const int i = 32 * q + 2 * e;
+                float2 x = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, at2));
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                sum[e & 1] = add2(sum[e & 1], pack2(x.x, x.y));
+                const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
+                w[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              tmem_st_32x32b_x16(s_addr + 64 + 32 * half + 16 * q, w);
             }
-            tmem_st_32x32b_x16(s_addr + 16 * i, w);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          };
+          weights(s, 1);
+          tmem_load_64(s_addr, s);
+          if (masked) mask(s, left);
+          weights(s, 0);
+          const float2 sums = unpack2(add2(sum[0], sum[1]));
+          l += sums.x + sums.y;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -589,13 +671,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
     }
   }
   // the matrix instructions in flight land before the tensor memory is given back
-  if (warp == 12) {
+  if (warp == 15) {
     if (elect_one_sync()) tc_commit(&sh.drain);
     __syncwarp();
     warp_wait(&sh.drain, 0, timeout, nullptr, kSiteDrain);
   }
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 15) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace fp8mm
