@@ -315,28 +315,6 @@ struct PreValues {
   }
 };
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAttnArgs p) {
   using Cfg = PreCfg<D>;
@@ -537,11 +515,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           auto top = [](const uint32_t (&s)[64]) {
             float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
 #pragma unroll
-            for (int e = 2; e < 64; e += 2) {
-              a = fmaxf(a, __uint_as_float(s[e]));
-              b = fmaxf(b, __uint_as_float(s[e + 1]));
+            for (int e = 2; e < 62; e += 4) {
+              a = fmaxf(fmaxf(a, __uint_as_float(s[e])), __uint_as_float(s[e + 1]));
+              b = fmaxf(fmaxf(b, __uint_as_float(s[e + 2])), __uint_as_float(s[e + 3]));
             }
-            return fmaxf(a, b);
+            return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(s[62]), __uint_as_float(s[63])));
           };
           // the first half of the scores is read twice (for the maximum, for
           // the weights), the second half stays in registers
@@ -575,8 +553,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
             tmem_st_wait();
           }
           const float at = m == -INFINITY ? 0.f : m;
-          const uint64_t sc2 = pack2(sc, sc), at2 = pack2(-at, -at);
-          uint64_t sum[2] = {0, 0};
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
           // 64 weights of s to 32 columns; the place is free: S's second half has been read
           auto weights = [&](const uint32_t (&s)[64], int half) {
 #pragma unroll
@@ -585,11 +562,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const int i = 32 * q + 2 * e;
-                float2 x = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, at2));
-                x.x = ex2(x.x);
-                x.y = ex2(x.y);
-                sum[e & 1] = add2(sum[e & 1], pack2(x.x, x.y));
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
+                const float x = ex2(fmaf(__uint_as_float(s[i]), sc, -at)), y = ex2(fmaf(__uint_as_float(s[i + 1]), sc, -at));
+                sum[2 * (e & 1)] += x;
+                sum[2 * (e & 1) + 1] += y;
+                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
                 w[e] = *reinterpret_cast<const uint32_t*>(&v);
               }
               tmem_st_32x32b_x16(s_addr + 64 + 32 * half + 16 * q, w);
@@ -599,8 +575,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           tmem_load_64(s_addr, s);
           if (masked) mask(s, left);
           weights(s, 0);
-          const float2 sums = unpack2(add2(sum[0], sum[1]));
-          l += sums.x + sums.y;
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
