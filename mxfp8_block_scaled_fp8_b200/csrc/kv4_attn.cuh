@@ -130,8 +130,9 @@ __device__ __forceinline__ float scale2(float x, int n) {
 // ------------------------------------------------------------------ the plan
 
 // What laying a tile out costs a warp, in steps (each short tile of a batch
-// adds its latency: queries, page table, first records, results).
-constexpr int kTileSteps = 4;
+// adds its latency: queries, page table, first records, results).  64 sequences
+// of 1 to 8192 tokens: 92.6 us with 2, 73.6 with 4, 68.3 with 6, 68.8 with 10.
+constexpr int kTileSteps = 6;
 
 struct AttnSeq {
   int lo, n, len;

@@ -4,22 +4,30 @@
 // The arithmetic of kv4_attn.cuh for tiles of 256 rows (query tokens x the
 // heads that share a key/value head), two halves of 128, the TMEM lanes:
 //   S = Q K^T       Q, K bf16 in shared memory, fp32 in TMEM
-//   P = 2^(S scale log2 e - m), bf16, written over the second half of S
+//   P = 2^(S scale log2 e - m), bf16, written over S
 //   O += P V        P from TMEM, V^T bf16 in shared memory, fp32 in TMEM
 // Codes become bf16 exactly (a code has two significant bits, the exponent is
 // bf16's), so keys and values enter without error and without a range limit;
-// weights are rounded to 8 bits, and the row's sum is of the fp32 weights.  A
-// row's maximum moves only when a score passes it by 2^8, and O is scaled
-// then.
+// weights are rounded to 8 bits, and the row's sum is of the fp32 weights.
 //
 // Warps: 0-3 and 4-7 the softmax of the two halves (a thread per row), 8-10
 // bring keys and 11-14 values and write them as bf16 tiles, 15 issues the
-// matrix instructions.  Order on the tensor pipe: PV of a half, then QK of its next
-// tile, in turns, so that one half's softmax runs beside the other's products.
+// matrix instructions.  A step is 64 tokens; its scores have two places in
+// TMEM per half, so that the products fill one while the softmax is at the
+// other.  Keys and values have a ring of four steps each, freed apart: a key
+// tile after its QK, a value tile after its PV.
 //
-// Bounds of a tile of 128 tokens (256 rows, D = 128), in SM clocks: tensor
-// 2048, exponentials 2048, shared memory 2048 (the products read 128 bytes a
-// clock of it).
+// Bounds of a step (256 rows, D = 128), in SM clocks: tensor 1290 (PV 8 x 64;
+// QK 16 x 48.6, because its operands' 6 KB pass shared memory at 128 bytes a
+// clock), exponentials 1024, writing tiles 400 of shared memory's clocks.
+// Measured on two prompts' chunks of 1025 to 2048 tokens in contexts of up to
+// 16384, 32 heads on 8 (541 GFLOP): 627 us, 863 TFLOP/s, 52 % of the rate that a
+// plain bf16 GEMM reaches here.  What was tried on the way, same work: steps
+// of 128 tokens with one place for scores 871 us (the softmax waits for its
+// own products); with scores double buffered but tiles of 128 tokens freed
+// whole 918 us (conversion in the chain); steps of 128 tokens whose products
+// are issued as they are ready 713 us (the tensor pipe takes an instruction
+// only when the one before is under way, so turns of the two halves collide).
 //
 // Work split: as in kv4_attn.cuh, a job per CTA in a line of costs, which here
 // follow the causal mask; cut tiles are joined by the same second kernel.
@@ -30,22 +38,25 @@
 namespace fp8mm {
 
 constexpr int kPreRows = 256;        // rows of a tile
-constexpr int kPreTokens = 128;      // tokens of a step
-constexpr int kPreStages = 2;
+constexpr int kPreTokens = 64;       // tokens of a step
+constexpr int kPreGroups = kPreTokens / kGroup;
+constexpr int kPreStages = 4;        // steps whose keys, and whose values, have a place in shared memory
 constexpr int kPreThreads = 512;
-constexpr int kPreKeyWarps = 3, kPreValueWarps = 4;  // that write key and value tiles: 8 groups of a step each
+constexpr int kPreKeyWarps = 3, kPreValueWarps = 4;  // that write key and value tiles
 constexpr float kPreSlack = 8.f;
-constexpr int kPreTileCost = 4;      // what a tile costs beside its tokens, in units of 64 tokens
-constexpr uint32_t kIdescBf16 = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kPreTokens >> 4) << 24);
+// What a tile costs beside its tokens, in units of 64 tokens (queries to shared
+// memory, the chain's fill and drain, the rows' store): with 4 the jobs of many
+// short tiles ran 20 % longer than others (740 us), 7: 665, 9: 640, 11: 627, 13: 628.
+constexpr int kPreTileCost = 11;
+constexpr uint32_t kIdescBf16 = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4 << 24);
 
 template <int D>
 struct PreCfg {
-  static constexpr int kBlock = 128 * 128;               // 128 rows of 64 bf16
+  static constexpr int kQBlock = 128 * 128;              // 128 rows of 64 bf16
+  static constexpr int kKBlock = kPreTokens * 128;
   static constexpr int kQBytes = kPreRows * D * 2;
-  static constexpr int kKBytes = kPreTokens * D * 2;     // D / 64 blocks of 128 rows
-  static constexpr int kVBytes = D * kPreTokens * 2;     // two blocks of D rows
-  static constexpr int kStageBytes = kKBytes + kVBytes;
-  static constexpr int kSmemBytes = kQBytes + kPreStages * kStageBytes + 1024;  // tiles stand on 1024-byte boundaries
+  static constexpr int kTileBytes = kPreTokens * D * 2;  // of keys: D / 64 blocks; of values: one block of D rows
+  static constexpr int kSmemBytes = kQBytes + 2 * kPreStages * kTileBytes + 1024;  // tiles stand on 1024-byte boundaries
 };
 
 // kind::f16 products, A from shared memory or from TMEM.
@@ -70,7 +81,7 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, 
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),       \
       "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),      \
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-// 32 columns of this thread's lane, loaded and waited for in one statement, so
+// Columns of this thread's lane, loaded and waited for in one statement, so
 // that no register is touched before it holds its value.
 __device__ __forceinline__ void tmem_load_32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -101,7 +112,16 @@ __device__ __forceinline__ void tmem_load_64(uint32_t taddr, uint32_t (&r)[64]) 
       : "r"(taddr)
       : "memory");
 }
-// 32 and 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_load_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Stores of this thread's lane.
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -147,7 +167,7 @@ __device__ __forceinline__ int64_t pre_cost(const KvAttnArgs& p, const PreSeq& q
 struct PrePiece {
   PreSeq q;
   int s, head, row0;
-  int k0, k1;              // steps of 128 tokens
+  int k0, k1;              // steps
   int64_t base;            // units before sequence s
   int64_t i0, i1, u, end;  // units of the tile; of the piece
   int64_t job_u, job_end;
@@ -219,8 +239,8 @@ template <int D>
 struct PreShared {
   PrePlan plan;
   PrePiece piece;
-  uint64_t kv_full[kPreStages], kv_empty[kPreStages];
-  uint64_t s_full[2], p_full[2], pv_done[2], drain;
+  uint64_t full[2][kPreStages], empty[2][kPreStages];  // of keys, of values
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], drain;
   uint32_t tmem;
   int abort;
 };
@@ -259,9 +279,11 @@ struct PreKeys {
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int row = at * kGroup + g + 8 * h, chunk = (b & 1) * 4 + c;
-        *reinterpret_cast<uint4*>(tile + (b >> 1) * PreCfg<D>::kBlock + row * 128 + ((chunk ^ g) << 4)) =
-            e2m1x8_to_bf16(w[h][b], ue8m0_to_f32((e[h] >> (8 * b)) & 0xFFu));
+        // rows of odd g take the other half of their 128 bytes: the 8 lanes
+        // of a phase meet all banks
+        const int odd = (b ^ g) & 1, row = at * kGroup + g + 8 * h, chunk = odd * 4 + c;
+        *reinterpret_cast<uint4*>(tile + (b >> 1) * PreCfg<D>::kKBlock + row * 128 + ((chunk ^ g) << 4)) =
+            e2m1x8_to_bf16(odd ? w[h][b | 1] : w[h][b & ~1], ue8m0_to_f32((e[h] >> (8 * ((b & ~1) + odd))) & 0xFFu));
       }
   }
 };
@@ -290,7 +312,7 @@ struct PreValues {
       if (base + t < len) e[i] = load_exponents<NB>(rec + 16 * D + D / 2 + t * NB);
     }
   }
-  // Into the tile [d][token]: blocks of 64 tokens, swizzled rows as the keys'.
+  // Into the tile [d][token], swizzled rows as the keys'.
   __device__ __forceinline__ void store(uint8_t* tile, int at) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -306,8 +328,8 @@ struct PreValues {
         for (int i = 0; i < 4; ++i) {
           const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
           const __nv_bfloat162 r = __floats2bfloat162_rn(v.x * f[2 * (i >> 1)], v.y * f[2 * (i >> 1) + 1]);
-          const int d = 16 * j + g + 8 * (i & 1), chunk = 2 * (at & 3) + (i >> 1);
-          *reinterpret_cast<uint32_t*>(tile + (at >> 2) * (D * 128) + d * 128 + ((chunk ^ g) << 4) + 4 * c) =
+          const int d = 16 * j + g + 8 * (i & 1), chunk = 2 * at + (i >> 1);
+          *reinterpret_cast<uint32_t*>(tile + d * 128 + ((chunk ^ g) << 4) + 4 * c) =
               *reinterpret_cast<const uint32_t*>(&r);
         }
       }
@@ -326,13 +348,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
   volatile int* abort = &sh.abort;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPreStages; ++i) {
-      mbar_init(&sh.kv_full[i], kPreKeyWarps + kPreValueWarps);
-      mbar_init(&sh.kv_empty[i], 1);
+      for (int v = 0; v < 2; ++v) {
+        mbar_init(&sh.full[v][i], kPreGroups);
+        mbar_init(&sh.empty[v][i], 1);
+      }
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
-      mbar_init(&sh.pv_done[i], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sh.s_full[i][b], 1);
+        mbar_init(&sh.p_full[i][b], 4);
+        mbar_init(&sh.pv_done[i][b], 1);
+      }
     }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
@@ -351,9 +377,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
   const int64_t total = sh.plan.before[kAttnThreads];
   const int64_t jobs = min(static_cast<int64_t>(gridDim.x), total);
   const uint64_t timeout = p.timeout_ns;
-  // registers: 512 threads at 128 become 256 at 160 (softmax) and 256 at 96
-  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   uint32_t tile0 = 0;  // steps of earlier pieces
 
   if (blockIdx.x < jobs) {
@@ -393,7 +416,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const int i = threadIdx.x + j * kPreThreads, r = i / (D / 8), ch = i % (D / 8);
-          *reinterpret_cast<uint4*>(qs + (r >> 7) * (128 * D * 2) + (ch >> 3) * Cfg::kBlock + (r & 127) * 128 +
+          *reinterpret_cast<uint4*>(qs + (r >> 7) * (128 * D * 2) + (ch >> 3) * Cfg::kQBlock + (r & 127) * 128 +
                                     (((ch & 7) ^ (r & 7)) << 4)) =
               make_uint4(v[j].x ^ sign, v[j].y ^ sign, v[j].z ^ sign, v[j].w ^ sign);
         }
@@ -402,91 +425,92 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
       __syncthreads();
 
       if (warp >= 8 && warp < 15) {
-        // ---- records to bf16 tiles, a step ahead in registers
-        const int groups = (len + kGroup - 1) / kGroup, seq = pc.s;
-        // this warp's groups of a step: first, first + warps, .. < 8; one is
+        // ---- records to bf16 tiles
+        const int groups = (len + kGroup - 1) / kGroup, seq = pc.s, units = (k1 - k0) * kPreGroups;
+        // this warp's groups of the piece: first, first + warps, ..; one is
         // written while the next is on its way
-        auto bring = [&](auto rec, int first, int warps, int offset) {
-          const int per = (8 - first + warps - 1) / warps, units = (k1 - k0) * per;
-          uint64_t addr = 0;  // lane i: the record of unit 32 n + i
-          auto load = [&](int unit) {
-            if ((unit & 31) == 0) {
-              const int u = unit + lane, group = (k0 + u / per) * 8 + first + u % per * warps;
+        auto bring = [&](auto rec, int which, int first, int warps) {
+          uint64_t addr = 0;  // lane i: the record of the warp's group 32 n + i
+          auto load = [&](int n) {
+            const int unit = first + n * warps;
+            if ((n & 31) == 0) {
+              const int u = unit + lane * warps, group = k0 * kPreGroups + u;
               addr = u < units && group < groups ? reinterpret_cast<uint64_t>(kv_record<D>(p.kv, seq, group, head)) : 0;
             }
-            const uint64_t a = __shfl_sync(0xFFFFFFFFu, addr, unit & 31);
-            rec.load(reinterpret_cast<const uint8_t*>(a), ((k0 + unit / per) * 8 + first + unit % per * warps) * kGroup, len);
+            const uint64_t a = __shfl_sync(0xFFFFFFFFu, addr, n & 31);
+            rec.load(reinterpret_cast<const uint8_t*>(a), (k0 * kPreGroups + unit) * kGroup, len);
           };
-          if (units > 0) load(0);
+          if (first < units) load(0);
 #pragma unroll 1
-          for (int unit = 0; unit < units; ++unit) {
-            const int step = unit / per, i = unit - step * per;
-            const uint32_t it = tile0 + step;
+          for (int unit = first, n = 0; unit < units; unit += warps, ++n) {
+            const uint32_t it = tile0 + unit / kPreGroups;
             const int st = it % kPreStages;
             auto cur = rec;
-            if (unit + 1 < units) load(unit + 1);
-            if (i == 0 && !warp_wait(&sh.kv_empty[st], ((it / kPreStages) & 1) ^ 1, timeout, abort, kSiteKvRecord)) break;
-            cur.store(smem + Cfg::kQBytes + st * Cfg::kStageBytes + offset, first + i * warps);
-            if (i == per - 1) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.kv_full[st]);
-            }
+            if (unit + warps < units) load(n + 1);
+            if (!warp_wait(&sh.empty[which][st], ((it / kPreStages) & 1) ^ 1, timeout, abort, kSiteKvRecord)) break;
+            cur.store(smem + Cfg::kQBytes + (which * kPreStages + st) * Cfg::kTileBytes, unit % kPreGroups);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.full[which][st]);
           }
         };
         if (warp < 8 + kPreKeyWarps)
-          bring(PreKeys<D>(), warp - 8, kPreKeyWarps, 0);
+          bring(PreKeys<D>(), 0, warp - 8, kPreKeyWarps);
         else
-          bring(PreValues<D>(), warp - 8 - kPreKeyWarps, kPreValueWarps, Cfg::kKBytes);
+          bring(PreValues<D>(), 1, warp - 8 - kPreKeyWarps, kPreValueWarps);
       } else if (warp == 15) {
         // ---- products
         const uint32_t idesc_s = kIdescBf16 | (static_cast<uint32_t>(kPreTokens >> 3) << 17);
         const uint32_t idesc_o = kIdescBf16 | (static_cast<uint32_t>(D >> 3) << 17);
-        const uint32_t q_addr = smem_u32(qs), kv_addr = smem_u32(smem + Cfg::kQBytes);
+        // an address takes 16-byte steps in a descriptor's low bits
+        const uint64_t q_desc = sw128_kmajor_desc(smem_u32(qs)), k_desc = q_desc + Cfg::kQBytes / 16;
+        const uint64_t v_desc = k_desc + kPreStages * Cfg::kTileBytes / 16;
         auto qk = [&](int t, uint32_t it) {
           if (elect_one_sync()) {
-            const uint32_t kb = kv_addr + (it % kPreStages) * Cfg::kStageBytes;
+            const uint64_t qd = q_desc + t * (128 * D * 2 / 16), kd = k_desc + it % kPreStages * (Cfg::kTileBytes / 16);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const uint32_t off = (i >> 2) * Cfg::kBlock + (i & 3) * 32;
-              mma_bf16_ss(tmem + 128 * t, sw128_kmajor_desc(q_addr + t * (128 * D * 2) + off),
-                          sw128_kmajor_desc(kb + off), idesc_s, i != 0);
-            }
-            tc_commit(&sh.s_full[t]);
+            for (int i = 0; i < D / 16; ++i)
+              mma_bf16_ss(tmem + 128 * t + 64 * (it & 1), qd + (i >> 2) * (Cfg::kQBlock / 16) + (i & 3) * 2,
+                          kd + (i >> 2) * (Cfg::kKBlock / 16) + (i & 3) * 2, idesc_s, i != 0);
+            tc_commit(&sh.s_full[t][it & 1]);
+            if (t == 1) tc_commit(&sh.empty[0][it % kPreStages]);
           }
           __syncwarp();
         };
-        bool ok = k0 >= k1 || warp_wait(&sh.kv_full[tile0 % kPreStages], (tile0 / kPreStages) & 1, timeout, abort, kSiteMmaFull);
-        if (ok && k0 < k1) {
+        auto there = [&](int which, uint32_t it) {
+          const bool ok = warp_wait(&sh.full[which][it % kPreStages], (it / kPreStages) & 1, timeout, abort, kSiteMmaFull);
           tc_fence_after();
-          qk(0, tile0);
-          qk(1, tile0);
+          return ok;
+        };
+        const uint32_t it0 = tile0, it1 = tile0 + (k1 - k0);
+        bool ok = true;
+        for (uint32_t it = it0; it < min(it0 + 2, it1) && ok; ++it) {
+          ok = there(0, it);
+          if (!ok) break;
+          qk(0, it);
+          qk(1, it);
         }
-        for (int k = k0; k < k1 && ok; ++k) {
-          const uint32_t it = tile0 + (k - k0);
-          const int st = it % kPreStages;
-          const uint32_t vb = kv_addr + st * Cfg::kStageBytes + Cfg::kKBytes;
+        for (uint32_t it = it0; it < it1 && ok; ++it) {
+          const uint64_t vd = v_desc + it % kPreStages * (Cfg::kTileBytes / 16);
+          const uint32_t more = it != it0;
+          ok = there(1, it);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            ok = ok && warp_wait(&sh.p_full[t], it & 1, timeout, abort, kSiteMmaAccEmpty);
+            ok = ok && warp_wait(&sh.p_full[t][it & 1], (it >> 1) & 1, timeout, abort, kSiteMmaAccEmpty);
             if (!ok) break;
             tc_fence_after();
             if (elect_one_sync()) {
 #pragma unroll
               for (int i = 0; i < kPreTokens / 16; ++i)
-                mma_bf16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 64 + 8 * i,
-                            sw128_kmajor_desc(vb + (i >> 2) * (D * 128) + (i & 3) * 32), idesc_o, k != k0 || i != 0);
-              tc_commit(&sh.pv_done[t]);
-              if (t == 1) tc_commit(&sh.kv_empty[st]);
+                mma_bf16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 64 * (it & 1) + 8 * i, vd + 2 * i, idesc_o, i != 0 ? 1u : more);
+              tc_commit(&sh.pv_done[t][it & 1]);
+              if (t == 1) tc_commit(&sh.empty[1][it % kPreStages]);
             }
             __syncwarp();
-            if (k + 1 < k1) {
-              if (t == 0) {
-                ok = warp_wait(&sh.kv_full[(it + 1) % kPreStages], ((it + 1) / kPreStages) & 1, timeout, abort, kSiteMmaFull);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              qk(t, it + 1);
+            if (it + 2 < it1) {
+              if (t == 0) ok = there(0, it + 2);
+              if (!ok) break;
+              qk(t, it + 2);
             }
           }
         }
@@ -500,90 +524,86 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
         const float sc = fabsf(p.scale_log2);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int k = k0; k < k1; ++k) {
-          const uint32_t it = tile0 + (k - k0);
-          ok = warp_wait(&sh.s_full[t], it & 1, timeout, abort, kSiteEpiAccFull);
+        const uint32_t it0 = tile0, it1 = tile0 + (k1 - k0);
+        for (uint32_t it = it0; it < it1; ++it) {
+          ok = warp_wait(&sh.s_full[t][it & 1], (it >> 1) & 1, timeout, abort, kSiteEpiAccFull);
           if (!ok) break;
           tc_fence_after();
-          const int left = vis - k * kPreTokens;  // tokens of the step that the row sees
+          const uint32_t buf = s_addr + 64 * (it & 1);
+          const int left = vis - (k0 + static_cast<int>(it - it0)) * kPreTokens;  // tokens of the step that the row sees
           const bool masked = __any_sync(0xFFFFFFFFu, left < kPreTokens);
-          auto mask = [](uint32_t (&s)[64], int left) {
+          // The maximum only keeps weights and sums in fp32's range (a bf16
+          // weight has 8 bits at any size), so a step is not searched for it:
+          // the rows' first sets it, and one whose weights sum to more than
+          // 2^40 is taken again with a new one.
+          bool search = __any_sync(0xFFFFFFFFu, it == it0 || (m == -INFINITY && left > 0));
+          uint32_t w[32];
+          while (true) {
+            uint32_t s[64];
+            tmem_load_64(buf, s);
+            if (masked) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (e >= left) s[e] = 0xFF800000u;
-          };
-          auto top = [](const uint32_t (&s)[64]) {
-            float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
-#pragma unroll
-            for (int e = 2; e < 62; e += 4) {
-              a = fmaxf(fmaxf(a, __uint_as_float(s[e])), __uint_as_float(s[e + 1]));
-              b = fmaxf(fmaxf(b, __uint_as_float(s[e + 2])), __uint_as_float(s[e + 3]));
+              for (int e = 0; e < 64; ++e)
+                if (e >= left) s[e] = 0xFF800000u;
             }
-            return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(s[62]), __uint_as_float(s[63])));
-          };
-          // the first half of the scores is read twice (for the maximum, for
-          // the weights), the second half stays in registers
-          uint32_t s[64];
-          tmem_load_64(s_addr, s);
-          if (masked) mask(s, left);
-          float mx = top(s);
-          tmem_load_64(s_addr + 64, s);
-          if (masked) mask(s, left - 64);
-          mx = fmaxf(mx, top(s));
-          mx *= sc;
-          float f = 1.f;
-          if (mx > m + kPreSlack || (m == -INFINITY && mx != -INFINITY)) {
-            f = ex2(m - mx);
-            m = mx;
-            l *= f;
-          }
-          if (__any_sync(0xFFFFFFFFu, f != 1.f) && k != k0) {
-            // scale what is summed; the products of the step before have landed first
-            ok = warp_wait(&sh.pv_done[t], (it & 1) ^ 1, timeout, abort, kSiteEpiSync);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t o[32];
-              tmem_load_32(o_addr + 32 * i, o);
+            if (search) {
+              float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_32x32b_x32(o_addr + 32 * i, o);
-            }
-            tmem_st_wait();
-          }
-          const float at = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          // 64 weights of s to 32 columns; the place is free: S's second half has been read
-          auto weights = [&](const uint32_t (&s)[64], int half) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int i = 32 * q + 2 * e;
-                const float x = ex2(fmaf(__uint_as_float(s[i]), sc, -at)), y = ex2(fmaf(__uint_as_float(s[i + 1]), sc, -at));
-                sum[2 * (e & 1)] += x;
-                sum[2 * (e & 1) + 1] += y;
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-                w[e] = *reinterpret_cast<const uint32_t*>(&v);
+              for (int e = 2; e < 64; e += 2) {
+                a = fmaxf(a, __uint_as_float(s[e]));
+                b = fmaxf(b, __uint_as_float(s[e + 1]));
               }
-              tmem_st_32x32b_x16(s_addr + 64 + 32 * half + 16 * q, w);
+              const float mx = fmaxf(a, b) * sc;
+              float f = 1.f;
+              if (mx > m + kPreSlack || (m == -INFINITY && mx != -INFINITY)) {
+                f = ex2(m - mx);
+                m = mx;
+                l *= f;
+              }
+              if (__any_sync(0xFFFFFFFFu, f != 1.f) && it != it0) {
+                // scale what is summed; the products of the step before have landed first
+                ok = warp_wait(&sh.pv_done[t][(it - 1) & 1], ((it - 1) >> 1) & 1, timeout, abort, kSiteEpiSync);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int i = 0; i < D / 16; ++i) {
+                  uint32_t o[16];
+                  tmem_load_16(o_addr + 16 * i, o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st_32x32b_x16(o_addr + 16 * i, o);
+                }
+                tmem_st_wait();
+              }
             }
-          };
-          weights(s, 1);
-          tmem_load_64(s_addr, s);
-          if (masked) mask(s, left);
-          weights(s, 0);
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float at = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = ex2(fmaf(__uint_as_float(s[2 * e]), sc, -at));
+              const float y = ex2(fmaf(__uint_as_float(s[2 * e + 1]), sc, -at));
+              sum[2 * (e & 1)] += x;
+              sum[2 * (e & 1) + 1] += y;
+              const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+              w[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (!search && __any_sync(0xFFFFFFFFu, !(all <= 0x1p40f))) {
+              search = true;
+              continue;
+            }
+            l += all;
+            break;
+          }
+          if (!ok) break;
+          tmem_st_32x32b_x32(buf, w);  // over the scores, which have been read
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_full[t]);
+          if (lane == 0) mbar_arrive(&sh.p_full[t][it & 1]);
         }
         // ---- the rows, or the piece's partial result
-        const uint32_t last = tile0 + (k1 - k0) - 1;
-        if (ok && k0 < k1) ok = warp_wait(&sh.pv_done[t], last & 1, timeout, abort, kSiteEpiSync);
+        if (ok && k0 < k1) ok = warp_wait(&sh.pv_done[t][(it1 - 1) & 1], ((it1 - 1) >> 1) & 1, timeout, abort, kSiteEpiSync);
         if (ok) {
           tc_fence_after();
           const bool row = rho < rows;
