@@ -408,7 +408,9 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
  *   out[r, h] = sum_j softmax_j(scale <q[r, h], k[j, h / g]>) v[j, h / g],  j <= position of row r,
  * g = q_heads / kv_heads, row i of sequence s's n rows at position seq_lens[s] - n + i (append first, then
  * attend).  A row that sees no token (seq_lens[s] == 0, or a position below 0) gives zeros.  Scores, softmax
- * statistics and sums are fp32; queries enter exactly, weights with 11 bits.
+ * statistics and sums are fp32; queries enter exactly, weights with 11 bits, or 8 in a call with a workspace and
+ * 128 or more rows of a key/value head per sequence (rows / batch, rounded up, times g), whose products are
+ * bf16.  Rows of a sequence with a page id outside the pool are unspecified.
  *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned
  *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
  *        empty row
@@ -428,7 +430,7 @@ size_t mxfp4_kv_attention_workspace_bytes(int64_t head_dim);
  * captured graph keeps them).  Every id in [0, num_pages), each dst at most once and none of them a src
  * (FP8MM_ERR_SHAPE otherwise).
  *   pages  device; page p of layer l at l * layer_stride + p * page_stride bytes; page_bytes are copied;
- *          16-byte aligned, all three multiples of 16. */
+ *          16-byte aligned, all three multiples of 16; no two pages of any layers overlap. */
 fp8mm_status kv_copy_pages(void* pages, int64_t num_pages, int64_t page_bytes, int64_t page_stride, int64_t layers,
                            int64_t layer_stride, const int32_t* src, const int32_t* dst, int64_t moves, void* stream);
 

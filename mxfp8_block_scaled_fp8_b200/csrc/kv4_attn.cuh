@@ -164,31 +164,37 @@ __device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs& p, int s) {
 }
 
 // Units before each strip of sequences; strip i is [i * per, (i + 1) * per).
+// Rising bounds keep the total below 2^31 (the host chose unit_steps for it);
+// others, whose rows may count twice, are recorded and nothing is done.
 struct AttnPlan {
   uint32_t before[kAttnThreads + 1];
-  uint32_t warp_sum[kAttnWarps];
+  uint64_t warp_sum[kAttnWarps];
 };
 
 template <int R>
 __device__ __forceinline__ int attn_plan(const KvAttnArgs& p, AttnPlan& pl) {
   const int per = (p.batch + kAttnThreads - 1) / kAttnThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t sum = 0;
-  const int s1 = min(p.batch, static_cast<int>((threadIdx.x + 1) * per));
-  for (int s = threadIdx.x * per; s < s1; ++s) {
-    const AttnSeq q = attn_seq<R>(p, s);
-    sum += q.tiles * q.units;
+  uint64_t sum = 0;
+  const int s1 = static_cast<int>(min(static_cast<int64_t>(p.batch), static_cast<int64_t>(threadIdx.x + 1) * per));
+  for (int64_t s = static_cast<int64_t>(threadIdx.x) * per; s < s1; ++s) {
+    const AttnSeq q = attn_seq<R>(p, static_cast<int>(s));
+    sum += min(static_cast<uint64_t>(q.tiles) * q.units, uint64_t{1} << 32);
   }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+    const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
     if (lane >= o) sum += v;
   }
   if (lane == 31) pl.warp_sum[warp] = sum;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kAttnWarps; ++w) sum += w < warp ? pl.warp_sum[w] : 0u;
-  pl.before[threadIdx.x + 1] = sum;
+  if (threadIdx.x == kAttnThreads - 1 && sum > INT32_MAX) {
+    record_index_error(kSiteSequence);
+    sum = 0;
+  }
+  pl.before[threadIdx.x + 1] = static_cast<uint32_t>(sum);
   if (threadIdx.x == 0) pl.before[0] = 0;
   __syncthreads();
   return per;

@@ -173,6 +173,9 @@ struct PrePiece {
   int64_t job_u, job_end;
 };
 
+// Above what a call can ask for: the host lets rows * group * heads be 4e9 at
+// most, so there are 4e9 / 256 + 4e9 / 128 tiles, of 2^25 units.
+constexpr int64_t kPreMostUnits = int64_t{1} << 52;
 struct PrePlan {
   int64_t before[kAttnThreads + 1];
   int64_t warp_sum[kAttnThreads / 32];
@@ -183,10 +186,10 @@ __device__ __forceinline__ int pre_plan(const KvAttnArgs& p, PrePlan& pl) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t sum = 0;
   if (threadIdx.x < kAttnThreads) {
-    const int s1 = min(p.batch, static_cast<int>((threadIdx.x + 1) * per));
-    for (int s = threadIdx.x * per; s < s1; ++s) {
-      const PreSeq q = pre_seq(p, s);
-      sum += pre_cost(p, q, q.tiles) * p.kv.kv_heads;
+    const int s1 = static_cast<int>(min(static_cast<int64_t>(p.batch), static_cast<int64_t>(threadIdx.x + 1) * per));
+    for (int64_t s = static_cast<int64_t>(threadIdx.x) * per; s < s1; ++s) {
+      const PreSeq q = pre_seq(p, static_cast<int>(s));
+      sum = min(sum + min(pre_cost(p, q, q.tiles), kPreMostUnits / p.kv.kv_heads) * p.kv.kv_heads, kPreMostUnits);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -198,6 +201,10 @@ __device__ __forceinline__ int pre_plan(const KvAttnArgs& p, PrePlan& pl) {
   __syncthreads();
   if (threadIdx.x < kAttnThreads) {
     for (int w = 0; w < warp; ++w) sum += pl.warp_sum[w];
+    if (threadIdx.x == kAttnThreads - 1 && sum >= kPreMostUnits) {  // bounds that do not rise, whose rows count twice
+      record_index_error(kSiteSequence);
+      sum = 0;
+    }
     pl.before[threadIdx.x + 1] = sum;
     if (threadIdx.x == 0) pl.before[0] = 0;
   }
