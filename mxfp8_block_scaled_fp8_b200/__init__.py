@@ -28,6 +28,20 @@ splits); ``sf_to_canonical`` / ``sf_from_canonical`` convert scales to and
 from the row-major [rows, k / 32] tensor.  For activations of a few token
 rows, ``mxfp8_quantize_8x4`` writes the scales in the small-M layout (rows
 padded to 8 instead of 128) that ``mxfp8_gemm(..., sf_a_8x4=True)`` reads.
+
+Attention over a key/value cache in 4 bits (MXFP4, in pages), behind a QKV
+projection of either kind::
+
+    cache = torch.zeros(pages, fp8mm.mxfp4_kv_page_bytes(64, kv_heads, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(fp8mm.mxfp4_kv_attention_workspace_bytes(128), dtype=torch.uint8, device="cuda")
+    q, k = fp8mm.qk_norm_rope(q, k, cos_sin, positions, q_weight, k_weight)    # [tokens, heads, 128]
+    fp8mm.mxfp4_kv_append(k, v, cache, page_table, seq_lens, 64, cu_seqlens)   # seq_lens with the new tokens
+    o = fp8mm.mxfp4_kv_attention(q, cache, page_table, seq_lens, 64, cu_seqlens, workspace=ws)
+
+without ``cu_seqlens`` each sequence has one new token (a decode step);
+``mxfp4_kv_gather`` reads tokens back as bf16; ``KvPagePool`` keeps the pages'
+books and ``kv_copy_pages`` makes the copies that its forks and compactions ask
+for.
 """
 from .fp8mm import (  # noqa: F401
     Fp8mmError, KERNEL_AUTO, concat_mla_k, KERNEL_SMALL_M, KERNEL_TILED, KERNEL_TILED_1SM, KERNEL_TILED_2SM, KERNEL_TILED_1SM_N128, fp8_gemm, fp8_gemm_e4m3_out, fp8_quantize_rowwise,
@@ -38,3 +52,4 @@ from .fp8mm import (  # noqa: F401
     kv_copy_pages, mxfp4_kv_append, mxfp4_kv_attention, mxfp4_kv_attention_workspace_bytes, mxfp4_kv_gather,
     mxfp4_kv_page_bytes, qk_norm_rope,
 )
+from .kv_pages import KvPagePool  # noqa: F401
