@@ -222,15 +222,14 @@ __device__ __forceinline__ KvSpan span_of(const KvSpan& sp, int from) {
   return o;
 }
 
-// Quantizes a warp's group of keys or values.  Lane (g, c) = (lane / 4,
-// lane % 4) has the eighth c of every block of token slots g and g + 8: a
-// block's maximum is over four neighbouring lanes.
+// A warp's group of keys or values.  Lane (g, c) = (lane / 4, lane % 4) has the
+// eighth c of every block of token slots g and g + 8: a block's maximum is over
+// four neighbouring lanes.
 template <int D>
-__device__ __forceinline__ void quantize_group(const __nv_bfloat16* x, int64_t st, const KvSpan& sp, int lane,
-                                               uint32_t (&code)[2][D / 32], uint32_t (&e)[2][D / 32]) {
+__device__ __forceinline__ void load_group(const __nv_bfloat16* x, int64_t st, const KvSpan& sp, int lane,
+                                           uint4 (&v)[2][D / 32]) {
   constexpr int NB = D / 32;
   const int g = lane >> 2, c = lane & 3;
-  uint4 v[2][NB];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int slot = g + 8 * h;
@@ -240,6 +239,11 @@ __device__ __forceinline__ void quantize_group(const __nv_bfloat16* x, int64_t s
     for (int b = 0; b < NB; ++b)
       v[h][b] = ok ? ld_stream_16(row + 32 * b) : make_uint4(0, 0, 0, 0);
   }
+}
+template <int D>
+__device__ __forceinline__ void quantize_group(const uint4 (&v)[2][D / 32], uint32_t (&code)[2][D / 32],
+                                               uint32_t (&e)[2][D / 32]) {
+  constexpr int NB = D / 32;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -296,12 +300,15 @@ __global__ void __launch_bounds__(kKvThreads) kv4_append_kernel(const KvAppendAr
     const bool leads = kv_span(p.cu, p.batch, static_cast<int>(p.rows), block * kRows, kRows, p.lens, nullptr, &mine);
     for (unsigned todo = __ballot_sync(0xFFFFFFFFu, leads); todo != 0; todo &= todo - 1) {
       const KvSpan sp = span_of(mine, __ffs(todo) - 1);
+      uint4 kx[2][NB], vx[2][NB];
+      load_group<D>(p.k + head * p.k_sh, p.k_st, sp, lane, kx);
+      load_group<D>(p.v + head * p.v_sh, p.v_st, sp, lane, vx);
       uint8_t* rec = kv_record<D>(p.kv, sp.seq, sp.group, head);
       if (rec == nullptr) continue;
       const int g = lane >> 2, c = lane & 3;
       uint32_t code[2][NB], e[2][NB];
       // keys: every token's codes and exponents are its own bytes
-      quantize_group<D>(p.k + head * p.k_sh, p.k_st, sp, lane, code, e);
+      quantize_group<D>(kx, code, e);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int slot = g + 8 * h;
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_append_kernel(const KvAppendAr
         if (c == 0) store_exponents<NB>(rec + 16 * D + slot * NB, e[h]);
       }
       // values: exponents by token, codes through shared memory and an 8 x 8 transpose
-      quantize_group<D>(p.v + head * p.v_sh, p.v_st, sp, lane, code, e);
+      quantize_group<D>(vx, code, e);
       __syncwarp();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
