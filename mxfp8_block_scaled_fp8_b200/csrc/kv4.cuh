@@ -279,8 +279,10 @@ __device__ __forceinline__ uint32_t load_exponents(const uint8_t* src) {
 
 // One warp per (kRows rows, head): 1 where most rows lead a group (decode),
 // 16 for prompts.  Bound by HBM for long prompts (4 D bytes
-// in, 17 D / 16 bytes out per token and head) and by the latency of the index
-// loads for a decode step.  A group that is written only in part keeps the
+// in, 17 D / 16 bytes out per token and head; 8 prompts of 1 to 2047 tokens, 8
+// heads, written and read back: 23.4 us, 27.6 with the values' loads behind the
+// keys' conversion) and by the latency of the index loads for a decode step
+// (64 tokens 4.4 us).  A group that is written only in part keeps the
 // codes of its other tokens: values share bytes between neighbouring tokens,
 // so those words are merged with what the record held.
 template <int D, int kRows>
@@ -397,8 +399,8 @@ __device__ __forceinline__ void store_bf16x16(__nv_bfloat16* dst, const uint4& a
 }
 
 // One warp per (16 rows, head), 17 D bytes in, 4 D bytes per token out.
-// Bound by HBM (79 % of the bytes are the writes).  kWide: v's rows are
-// 32-byte aligned.
+// Bound by HBM (79 % of the bytes are the writes): 131072 tokens of 8 heads of
+// 128 in 110 us, 6.2 TB/s, 94 % of a copy.  kWide: v's rows are 32-byte aligned.
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kKvThreads) kv4_gather_kernel(const KvGatherArgs p) {
   constexpr int NB = D / 32;
@@ -482,7 +484,8 @@ constexpr int kCopyUnroll = 4;
 // One block per slice of kCopyThreads * kCopyUnroll vectors of one move's
 // page in one layer.  The moves come by value as kernel parameters, so that a
 // captured graph holds them; no destination is another move's source, so the
-// order does not matter.  Bound by HBM.
+// order does not matter.  Bound by HBM: 400 pages of 68 KB in 16 layers in 138
+// us, 6.5 TB/s, 99 % of a copy.
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_pages_kernel(const __grid_constant__ KvCopyArgs p,
                                                                      uint32_t slices) {
   griddep_launch_dependents();

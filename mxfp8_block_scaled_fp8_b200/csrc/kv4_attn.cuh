@@ -16,10 +16,19 @@
 // second kernel joins them in the order of the jobs.  The plan is made on the
 // device from the lengths, so nothing depends on a length that the host
 // guessed, and a captured graph follows the lengths in memory.
-// Measured on the way (4 contexts of 100003..131072 tokens, 8 heads): eight
-// warps of a CTA on one piece, joined through shared memory, 117 us; the same
-// with a warp that brings the records and one that joins results, 122 us (a
-// CTA waits for its slowest warp).
+// Bound by reading the cache, 17 D bytes per 16 tokens and head, once, and close
+// behind it by the conversions (two a clock and SM, 8 per record and lane of
+// each operand: the ALU pipe is 66 % busy).  Measured: 4 contexts of 100003 to
+// 131072 tokens, 32 heads on 8, 100 us, 77 % of the rate of a copy; 64 of 1 to
+// 8192 tokens 68 us, 64 %.  Measured on the way, the long contexts: eight warps
+// of a CTA on one piece, joined through shared memory, 117 us; the same with a
+// warp that brings the records and one that joins results, 122 us (a CTA waits
+// for its slowest warp).
+//
+// Matrix instructions on registers, not tcgen05: with 4 to 16 rows the product
+// is a hundredth of what the tensor cores give, and tcgen05 would want the codes
+// as bf16 tiles in shared memory, four times the record's bytes written and read
+// again; kv4_prefill.cuh does that where there are rows enough to pay for it.
 //
 // Arithmetic.  Keys and values stay in registers as the record holds them.
 // E2M1 -> f16 is one exact conversion per two codes; a 16-token group is the

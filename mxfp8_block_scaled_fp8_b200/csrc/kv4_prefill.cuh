@@ -11,23 +11,26 @@
 // weights are rounded to 8 bits, and the row's sum is of the fp32 weights.
 //
 // Warps: 0-3 and 4-7 the softmax of the two halves (a thread per row), 8-10
-// bring keys and 11-14 values and write them as bf16 tiles, 15 issues the
-// matrix instructions.  A step is 64 tokens; its scores have two places in
-// TMEM per half, so that the products fill one while the softmax is at the
-// other.  Keys and values have a ring of four steps each, freed apart: a key
-// tile after its QK, a value tile after its PV.
+// bring keys and 11-13 values and write them as bf16 tiles, 14 and 15 issue the
+// matrix instructions of a half each.  A step is 64 tokens; its scores have two
+// places in TMEM per half, so that the products fill one while the softmax is at
+// the other.  Keys and values have a ring of four steps each, freed apart: a key
+// tile after its QKs, a value tile after its PVs.  Every warp goes from piece to
+// piece on its own, ordered by the barriers of what it reads and writes.
 //
 // Bounds of a step (256 rows, D = 128), in SM clocks: tensor 1290 (PV 8 x 64;
 // QK 16 x 48.6, because its operands' 6 KB pass shared memory at 128 bytes a
 // clock), exponentials 1024, writing tiles 400 of shared memory's clocks.
 // Measured on two prompts' chunks of 1025 to 2048 tokens in contexts of up to
-// 16384, 32 heads on 8 (541 GFLOP): 627 us, 863 TFLOP/s, 52 % of the rate that a
-// plain bf16 GEMM reaches here.  What was tried on the way, same work: steps
-// of 128 tokens with one place for scores 871 us (the softmax waits for its
-// own products); with scores double buffered but tiles of 128 tokens freed
-// whole 918 us (conversion in the chain); steps of 128 tokens whose products
-// are issued as they are ready 713 us (the tensor pipe takes an instruction
-// only when the one before is under way, so turns of the two halves collide).
+// 16384, 32 heads on 8 (541 GFLOP): 618 us, 875 TFLOP/s, 53 % of the rate that a
+// plain bf16 GEMM reaches here; without the conversion to bf16 it would be 546,
+// without the exponentials 598, without both 500: what is left is the tensor pipe
+// beside the softmax's reads and writes of TMEM.  What was tried on the way,
+// same work: steps of 128 tokens with one place for scores 871 us (the softmax
+// waits for its own products); scores in two places but tiles of 128 tokens
+// freed whole 918 us (conversion in the chain); steps of 128 tokens whose
+// products are issued as they are ready 713 us; one issuing warp 627 us (its
+// waits are the tensor pipe's); four warps for values and two for keys 677 us.
 //
 // Work split: as in kv4_attn.cuh, a job per CTA in a line of costs, which here
 // follow the causal mask; cut tiles are joined by the same second kernel.
@@ -38,16 +41,17 @@
 namespace fp8mm {
 
 constexpr int kPreRows = 256;        // rows of a tile
+constexpr int kPreFrom = 96;         // rows of a head and sequence from which this kernel is the faster one (kv4.cu)
 constexpr int kPreTokens = 64;       // tokens of a step
 constexpr int kPreGroups = kPreTokens / kGroup;
 constexpr int kPreStages = 4;        // steps whose keys, and whose values, have a place in shared memory
 constexpr int kPreThreads = 512;
-constexpr int kPreKeyWarps = 3, kPreValueWarps = 4;  // that write key and value tiles
+constexpr int kPreKeyWarps = 3, kPreValueWarps = 3;  // that write key and value tiles
 constexpr float kPreSlack = 8.f;
 // What a tile costs beside its tokens, in units of 64 tokens (queries to shared
-// memory, the chain's fill and drain, the rows' store): with 4 the jobs of many
-// short tiles ran 20 % longer than others (740 us), 7: 665, 9: 640, 11: 627, 13: 628.
-constexpr int kPreTileCost = 11;
+// memory, the chain's fill and drain, the rows' store): 644 us with 6, 618 with
+// 8, 619 with 11.
+constexpr int kPreTileCost = 9;
 constexpr uint32_t kIdescBf16 = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4 << 24);
 
 template <int D>
@@ -166,9 +170,8 @@ __device__ __forceinline__ int64_t pre_cost(const KvAttnArgs& p, const PreSeq& q
 
 struct PrePiece {
   PreSeq q;
-  int s, head, row0;
-  int k0, k1;              // steps
-  int64_t base;            // units before sequence s
+  int s, head, tile;       // sequence, head, row tile
+  int row0, k0, k1;        // first row; steps
   int64_t i0, i1, u, end;  // units of the tile; of the piece
   int64_t job_u, job_end;
 };
@@ -212,32 +215,63 @@ __device__ __forceinline__ int pre_plan(const KvAttnArgs& p, PrePlan& pl) {
   return per;
 }
 
-// The piece that begins at unit pc.u, going on from sequence pc.s.  Within a
-// sequence the heads of a row tile stand side by side.
-__device__ __forceinline__ void pre_piece(const KvAttnArgs& p, PrePiece& pc) {
+// The piece's rows and its share of the tile's steps.
+__device__ __forceinline__ void pre_share(const KvAttnArgs& p, PrePiece& pc) {
+  pc.end = min(pc.job_end, pc.i1);
+  pc.row0 = pc.tile * kPreRows;
+  const int last = min(pc.row0 + kPreRows, pc.q.rows) - 1;
+  const int seen = max(pc.q.len - pc.q.n + last / p.group + 1, 0);
+  const int64_t steps = (seen + kPreTokens - 1) / kPreTokens, c = pc.i1 - pc.i0;
+  pc.k0 = pc.u == pc.i0 ? 0 : static_cast<int>((pc.u - pc.i0) * steps / c);
+  pc.k1 = static_cast<int>(pc.end == pc.i1 ? steps : (pc.end - pc.i0) * steps / c);
+}
+// A job's first piece.  Within a sequence the heads of a row tile stand side
+// by side.
+__device__ __forceinline__ void pre_first(const KvAttnArgs& p, const PrePlan& pl, int per, int64_t job, int64_t jobs,
+                                          int64_t total, PrePiece& pc) {
   const int heads = p.kv.kv_heads;
-  while (pc.u >= pc.base + pre_cost(p, pc.q, pc.q.tiles) * heads) {
-    pc.base += pre_cost(p, pc.q, pc.q.tiles) * heads;
+  pc.job_u = pc.u = job * total / jobs;
+  pc.job_end = (job + 1) * total / jobs;
+  int lo = 0, hi = min(kAttnThreads, (p.batch + per - 1) / per);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (pl.before[mid] <= pc.u) lo = mid; else hi = mid;
+  }
+  pc.s = lo * per;
+  int64_t base = pl.before[lo];
+  pc.q = pre_seq(p, pc.s);
+  for (int64_t c; pc.u >= base + (c = pre_cost(p, pc.q, pc.q.tiles) * heads);) {
+    base += c;
     pc.q = pre_seq(p, ++pc.s);
   }
-  const int64_t x = pc.u - pc.base;
-  int lo = 0, hi = pc.q.tiles;  // cost(lo) heads <= x < cost(hi) heads
+  const int64_t x = pc.u - base;
+  lo = 0, hi = pc.q.tiles;  // cost(lo) heads <= x < cost(hi) heads
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (pre_cost(p, pc.q, mid) * heads <= x) lo = mid; else hi = mid;
   }
   const int64_t c0 = pre_cost(p, pc.q, lo), c = pre_cost(p, pc.q, lo + 1) - c0;
+  pc.tile = lo;
   pc.head = static_cast<int>((x - c0 * heads) / c);
-  pc.i0 = pc.base + c0 * heads + pc.head * c;
+  pc.i0 = base + c0 * heads + pc.head * c;
   pc.i1 = pc.i0 + c;
-  pc.end = min(pc.job_end, pc.i1);
-  pc.row0 = lo * kPreRows;
-  const int last = min(pc.row0 + kPreRows, pc.q.rows) - 1;
-  const int seen = max(pc.q.len - pc.q.n + last / p.group + 1, 0);
-  const int64_t steps = (seen + kPreTokens - 1) / kPreTokens;
-  // the piece's share of the tile's steps
-  pc.k0 = static_cast<int>((pc.u - pc.i0) * steps / c);
-  pc.k1 = static_cast<int>((pc.end - pc.i0) * steps / c);
+  pre_share(p, pc);
+}
+// The next one: the next tile's beginning.
+__device__ __forceinline__ void pre_next(const KvAttnArgs& p, PrePiece& pc) {
+  int64_t c = pc.i1 - pc.i0;
+  if (++pc.head == p.kv.kv_heads) {
+    pc.head = 0;
+    ++pc.tile;
+    while (pc.tile >= pc.q.tiles) {
+      pc.q = pre_seq(p, ++pc.s);
+      pc.tile = 0;
+    }
+    c = pre_cost(p, pc.q, pc.tile + 1) - pre_cost(p, pc.q, pc.tile);
+  }
+  pc.u = pc.i0 = pc.i1;
+  pc.i1 = pc.i0 + c;
+  pre_share(p, pc);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -245,9 +279,9 @@ __device__ __forceinline__ void pre_piece(const KvAttnArgs& p, PrePiece& pc) {
 template <int D>
 struct PreShared {
   PrePlan plan;
-  PrePiece piece;
+  PrePiece piece[kPreThreads / 32];  // of each warp: they go from piece to piece on their own
   uint64_t full[2][kPreStages], empty[2][kPreStages];  // of keys, of values
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], drain;
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], drain;
   uint32_t tmem;
   int abort;
 };
@@ -357,17 +391,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
     for (int i = 0; i < kPreStages; ++i) {
       for (int v = 0; v < 2; ++v) {
         mbar_init(&sh.full[v][i], kPreGroups);
-        mbar_init(&sh.empty[v][i], 1);
+        mbar_init(&sh.empty[v][i], 2);
       }
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 4);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&sh.s_full[i][b], 1);
         mbar_init(&sh.p_full[i][b], 4);
         mbar_init(&sh.pv_done[i][b], 1);
       }
     }
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain, 2);
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -384,54 +419,46 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
   const int64_t total = sh.plan.before[kAttnThreads];
   const int64_t jobs = min(static_cast<int64_t>(gridDim.x), total);
   const uint64_t timeout = p.timeout_ns;
-  uint32_t tile0 = 0;  // steps of earlier pieces
+  uint32_t tile0 = 0;    // steps of earlier pieces
+  uint32_t filled = 0;   // earlier pieces that have steps
 
   if (blockIdx.x < jobs) {
-    if (threadIdx.x == 0) {
-      PrePiece& pc = sh.piece;
-      pc.job_u = pc.u = blockIdx.x * total / jobs;
-      pc.job_end = (blockIdx.x + 1) * total / jobs;
-      int lo = 0, hi = min(kAttnThreads, (p.batch + per - 1) / per);
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (sh.plan.before[mid] <= pc.u) lo = mid; else hi = mid;
-      }
-      pc.s = lo * per;
-      pc.base = sh.plan.before[lo];
-      pc.q = pre_seq(p, pc.s);
-      pre_piece(p, pc);
-    }
-    __syncthreads();
-    while (true) {
-      const PrePiece& pc = sh.piece;
-      const int row0 = pc.row0, rows = pc.q.rows, head = pc.head, len = pc.q.len, n = pc.q.n, k0 = pc.k0, k1 = pc.k1;
-      const bool whole = pc.u == pc.i0 && pc.end == pc.i1, begins = pc.i0 >= pc.job_u;
-      // queries, with the scale's sign, to shared memory
-      {
-        constexpr int N = kPreRows * D / 8 / kPreThreads;
-        uint4 v[N];
+    PrePiece& pc = sh.piece[warp];
+    if (lane == 0) pre_first(p, sh.plan, per, blockIdx.x, jobs, total, pc);
+    __syncwarp();
+    // A half's queries, with the scale's sign, to shared memory, by its softmax warps.
+    auto queries = [&](int t) {
+      constexpr int N = 128 * D / 8 / 128;
+      const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+      uint8_t* half = qs + t * (128 * D * 2);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int i = threadIdx.x + j * kPreThreads, r = i / (D / 8), ch = i % (D / 8);
+      for (int j0 = 0; j0 < N; j0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = (threadIdx.x & 127) + (j0 + j) * 128, rho = pc.row0 + 128 * t + i / (D / 8), ch = i % (D / 8);
           v[j] = make_uint4(0, 0, 0, 0);
-          if (row0 + r < rows) {
-            const int t = (row0 + r) / p.group, h = head * p.group + (row0 + r - t * p.group);
-            v[j] = ld_stream_16(p.q + static_cast<int64_t>(pc.q.lo + t) * p.q_st + h * p.q_sh + 8 * ch);
+          if (rho < pc.q.rows) {
+            const int tok = rho / p.group, h = pc.head * p.group + (rho - tok * p.group);
+            v[j] = ld_stream_16(p.q + static_cast<int64_t>(pc.q.lo + tok) * p.q_st + h * p.q_sh + 8 * ch);
           }
         }
-        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int i = threadIdx.x + j * kPreThreads, r = i / (D / 8), ch = i % (D / 8);
-          *reinterpret_cast<uint4*>(qs + (r >> 7) * (128 * D * 2) + (ch >> 3) * Cfg::kQBlock + (r & 127) * 128 +
-                                    (((ch & 7) ^ (r & 7)) << 4)) =
+        for (int j = 0; j < 8; ++j) {
+          const int i = (threadIdx.x & 127) + (j0 + j) * 128, r = i / (D / 8), ch = i % (D / 8);
+          *reinterpret_cast<uint4*>(half + (ch >> 3) * Cfg::kQBlock + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
               make_uint4(v[j].x ^ sign, v[j].y ^ sign, v[j].z ^ sign, v[j].w ^ sign);
         }
       }
       fence_proxy_async_smem();
-      __syncthreads();
-
-      if (warp >= 8 && warp < 15) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[t]);
+    };
+    if (warp < 8 && pc.k0 < pc.k1) queries(warp >> 2);
+    while (true) {
+      const int row0 = pc.row0, rows = pc.q.rows, head = pc.head, len = pc.q.len, n = pc.q.n, k0 = pc.k0, k1 = pc.k1;
+      const bool more = pc.end < pc.job_end;
+      if (warp >= 8 && warp < 14) {
         // ---- records to bf16 tiles
         const int groups = (len + kGroup - 1) / kGroup, seq = pc.s, units = (k1 - k0) * kPreGroups;
         // this warp's groups of the piece: first, first + warps, ..; one is
@@ -465,14 +492,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           bring(PreKeys<D>(), 0, warp - 8, kPreKeyWarps);
         else
           bring(PreValues<D>(), 1, warp - 8 - kPreKeyWarps, kPreValueWarps);
-      } else if (warp == 15) {
-        // ---- products
+      } else if (warp >= 14) {
+        // ---- products of a half
+        const int t = warp - 14;
         const uint32_t idesc_s = kIdescBf16 | (static_cast<uint32_t>(kPreTokens >> 3) << 17);
         const uint32_t idesc_o = kIdescBf16 | (static_cast<uint32_t>(D >> 3) << 17);
         // an address takes 16-byte steps in a descriptor's low bits
         const uint64_t q_desc = sw128_kmajor_desc(smem_u32(qs)), k_desc = q_desc + Cfg::kQBytes / 16;
         const uint64_t v_desc = k_desc + kPreStages * Cfg::kTileBytes / 16;
-        auto qk = [&](int t, uint32_t it) {
+        auto there = [&](int which, uint32_t it) {
+          return warp_wait(&sh.full[which][it % kPreStages], (it / kPreStages) & 1, timeout, abort, kSiteMmaFull);
+        };
+        auto qk = [&](uint32_t it) {
+          if (!there(0, it)) return false;
+          tc_fence_after();
           if (elect_one_sync()) {
             const uint64_t qd = q_desc + t * (128 * D * 2 / 16), kd = k_desc + it % kPreStages * (Cfg::kTileBytes / 16);
 #pragma unroll
@@ -480,46 +513,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
               mma_bf16_ss(tmem + 128 * t + 64 * (it & 1), qd + (i >> 2) * (Cfg::kQBlock / 16) + (i & 3) * 2,
                           kd + (i >> 2) * (Cfg::kKBlock / 16) + (i & 3) * 2, idesc_s, i != 0);
             tc_commit(&sh.s_full[t][it & 1]);
-            if (t == 1) tc_commit(&sh.empty[0][it % kPreStages]);
+            tc_commit(&sh.empty[0][it % kPreStages]);
           }
           __syncwarp();
-        };
-        auto there = [&](int which, uint32_t it) {
-          const bool ok = warp_wait(&sh.full[which][it % kPreStages], (it / kPreStages) & 1, timeout, abort, kSiteMmaFull);
-          tc_fence_after();
-          return ok;
+          return true;
         };
         const uint32_t it0 = tile0, it1 = tile0 + (k1 - k0);
-        bool ok = true;
-        for (uint32_t it = it0; it < min(it0 + 2, it1) && ok; ++it) {
-          ok = there(0, it);
-          if (!ok) break;
-          qk(0, it);
-          qk(1, it);
-        }
+        bool ok = k0 >= k1 || warp_wait(&sh.q_full[t], filled & 1, timeout, abort, kSiteMmaFull);
+        for (uint32_t it = it0; it < min(it0 + 2, it1) && ok; ++it) ok = qk(it);
         for (uint32_t it = it0; it < it1 && ok; ++it) {
-          const uint64_t vd = v_desc + it % kPreStages * (Cfg::kTileBytes / 16);
-          const uint32_t more = it != it0;
-          ok = there(1, it);
+          ok = there(1, it) && warp_wait(&sh.p_full[t][it & 1], (it >> 1) & 1, timeout, abort, kSiteMmaAccEmpty);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one_sync()) {
+            const uint64_t vd = v_desc + it % kPreStages * (Cfg::kTileBytes / 16);
+            const uint32_t more = it != it0;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            ok = ok && warp_wait(&sh.p_full[t][it & 1], (it >> 1) & 1, timeout, abort, kSiteMmaAccEmpty);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one_sync()) {
-#pragma unroll
-              for (int i = 0; i < kPreTokens / 16; ++i)
-                mma_bf16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 64 * (it & 1) + 8 * i, vd + 2 * i, idesc_o, i != 0 ? 1u : more);
-              tc_commit(&sh.pv_done[t][it & 1]);
-              if (t == 1) tc_commit(&sh.empty[1][it % kPreStages]);
-            }
-            __syncwarp();
-            if (it + 2 < it1) {
-              if (t == 0) ok = there(0, it + 2);
-              if (!ok) break;
-              qk(t, it + 2);
-            }
+            for (int i = 0; i < kPreTokens / 16; ++i)
+              mma_bf16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 64 * (it & 1) + 8 * i, vd + 2 * i, idesc_o, i != 0 ? 1u : more);
+            tc_commit(&sh.pv_done[t][it & 1]);
+            tc_commit(&sh.empty[1][it % kPreStages]);
           }
+          __syncwarp();
+          if (it + 2 < it1) ok = qk(it + 2);
         }
       } else {
         // ---- softmax: a thread per row
@@ -609,6 +625,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.p_full[t][it & 1]);
         }
+        const bool whole = pc.u == pc.i0 && pc.end == pc.i1, begins = pc.i0 >= pc.job_u;
+        const int lo = pc.q.lo;
+        if (!whole && begins && threadIdx.x == 0) {  // to the list of cut tiles
+          const int64_t last = (pc.i1 * jobs - 1) / total;  // the job that holds unit i1 - 1
+          p.cuts[atomicAdd(&p.counters->cut, 1u)] =
+              AttnCut{static_cast<int>(blockIdx.x), static_cast<int>(last), lo, head, row0, min(rows - row0, kPreRows)};
+        }
+        // ---- the next piece's queries: every QK of this one is done, since its scores have been read
+        if (more && ok) {
+          __syncwarp();
+          if (lane == 0) pre_next(p, pc);
+          __syncwarp();
+          if (pc.k0 < pc.k1) queries(t);
+        }
         // ---- the rows, or the piece's partial result
         if (ok && k0 < k1) ok = warp_wait(&sh.pv_done[t][(it1 - 1) & 1], ((it1 - 1) >> 1) & 1, timeout, abort, kSiteEpiSync);
         if (ok) {
@@ -618,7 +648,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           __nv_bfloat16* out = nullptr;
           const int tok = rho / p.group, h = head * p.group + (rho - tok * p.group);
           if (!whole) part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * (kPreRows * (D + 2));
-          else out = p.out + static_cast<int64_t>(pc.q.lo + tok) * p.o_st + h * p.o_sh;
+          else out = p.out + static_cast<int64_t>(lo + tok) * p.o_st + h * p.o_sh;
           const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
@@ -650,30 +680,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
             part[kPreRows * D + 128 * t + r] = m;
             part[kPreRows * D + kPreRows + 128 * t + r] = l;
           } else if (row && p.lse != nullptr) {
-            p.lse[static_cast<int64_t>(pc.q.lo + tok) * p.lse_st + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            p.lse[static_cast<int64_t>(lo + tok) * p.lse_st + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
           }
           tc_fence_before();
         }
       }
-      if (!whole && begins && threadIdx.x == 0) {  // to the list of cut tiles
-        const int64_t last = (pc.i1 * jobs - 1) / total;  // the job that holds unit i1 - 1
-        p.cuts[atomicAdd(&p.counters->cut, 1u)] =
-            AttnCut{static_cast<int>(blockIdx.x), static_cast<int>(last), pc.q.lo, head, row0, min(rows - row0, kPreRows)};
-      }
       tile0 += k1 - k0;
-      __syncthreads();
-      tc_fence_after();
-      if (pc.end >= pc.job_end || *abort != 0) break;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        sh.piece.u = sh.piece.end;
-        pre_piece(p, sh.piece);
+      filled += k0 < k1;
+      if (!more || *abort != 0) break;
+      if (warp >= 8) {
+        __syncwarp();
+        if (lane == 0) pre_next(p, pc);
+        __syncwarp();
       }
-      __syncthreads();
     }
   }
   // the matrix instructions in flight land before the tensor memory is given back
-  if (warp == 15) {
+  if (warp >= 14) {
     if (elect_one_sync()) tc_commit(&sh.drain);
     __syncwarp();
     warp_wait(&sh.drain, 0, timeout, nullptr, kSiteDrain);

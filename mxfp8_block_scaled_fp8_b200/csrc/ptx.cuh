@@ -25,7 +25,7 @@ enum WaitSite : unsigned {
   kSiteClusterReduce = 10,
   // data errors (kDevErrIndex): which index was out of range
   kSitePosition = 16, kSiteSequence = 17, kSitePage = 18,
-  kSiteKvRecord = 19, kSiteKvDrain = 20, kSiteKvPiece = 21, kSiteKvResult = 22,
+  kSiteKvRecord = 19, kSiteKvDrain = 20,
 };
 
 __device__ __forceinline__ void record_error(unsigned kind, unsigned site) {
@@ -63,19 +63,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Whether the phase with the given parity has completed; does not wait.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)

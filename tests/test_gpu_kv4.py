@@ -74,7 +74,7 @@ def _filled(rng, lengths, page_size, heads, dim, seed, make=_kv):
 
 # rows of a head per sequence, on average, from which the tcgen05 kernel runs (with a workspace); it rounds weights to
 # bf16 (2^-8 of each) where the other rounds them to f16
-MANY_ROWS, BF16_WEIGHTS = 128, 2.0 ** -8 + 2.0 ** -11
+MANY_ROWS, BF16_WEIGHTS = 96, 2.0 ** -8 + 2.0 ** -11
 
 
 def _check_attention(out, lse, q, cache, own, lengths, cu, scale, weights=2.0 ** -10):
