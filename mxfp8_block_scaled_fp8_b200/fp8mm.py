@@ -457,13 +457,18 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: torch.Tensor, positi
         kw = k_weight.data_ptr()
     if q_out is None:
         q_out = q.new_empty((t, hq, d))
+        qo = q_out.data_ptr(), hq * d, d
+    else:
+        qo = _heads(q_out, dev, "q_out", q.shape)
     if k_out is None:
         k_out = k.new_empty((t, hk, d))
+        ko = k_out.data_ptr(), hk * d, d
+    else:
+        ko = _heads(k_out, dev, "k_out", k.shape)
     cs = cos_sin.shape
     _check("qk_norm_rope", lib().qk_norm_rope(
         *qa, *ka, t, hq, hk, d, qw, kw, eps, cos_sin.data_ptr(), cs[0], cs[1], cos_sin.stride(0),
-        1 if interleaved else 0, positions.data_ptr(), *_heads(q_out, dev, "q_out", q.shape),
-        *_heads(k_out, dev, "k_out", k.shape), _raw(dev)))
+        1 if interleaved else 0, positions.data_ptr(), *qo, *ko, _raw(dev)))
     return q_out, k_out
 
 
@@ -528,10 +533,15 @@ def mxfp4_kv_gather(cache: torch.Tensor, page_table: torch.Tensor, cu_seqlens: t
     shape = (total, heads, head_dim)
     if k is None:
         k = cache.new_empty(shape, dtype=_BF16)
+        ka = k.data_ptr(), heads * head_dim, head_dim
+    else:
+        ka = _heads(k, dev, "k", shape)
     if v is None:
         v = cache.new_empty(shape, dtype=_BF16)
-    _check("mxfp4_kv_gather", lib().mxfp4_kv_gather(desc, st, cu_seqlens.data_ptr(), total, *_heads(k, dev, "k", shape),
-                                                    *_heads(v, dev, "v", shape), _raw(dev)))
+        va = v.data_ptr(), heads * head_dim, head_dim
+    else:
+        va = _heads(v, dev, "v", shape)
+    _check("mxfp4_kv_gather", lib().mxfp4_kv_gather(desc, st, cu_seqlens.data_ptr(), total, *ka, *va, _raw(dev)))
     return k, v
 
 
@@ -569,9 +579,12 @@ def mxfp4_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.T
         ws, wsb = workspace.data_ptr(), workspace.nbytes
     if out is None:
         out = q.new_empty((t, hq, d))
+        oa = out.data_ptr(), hq * d, d
+    else:
+        oa = _heads(out, dev, "out", q.shape)
     _check("mxfp4_kv_attention", lib().mxfp4_kv_attention(
         *qa, t, hq, cu, seq_lens.data_ptr(), desc, d ** -0.5 if scale is None else scale,
-        *_heads(out, dev, "out", q.shape), lp, lst, ws, wsb, _raw(dev)))
+        *oa, lp, lst, ws, wsb, _raw(dev)))
     return out
 
 

@@ -8,7 +8,7 @@ import torch
 
 import mxfp8_block_scaled_fp8_b200 as fp8mm
 from tests import gpu_util as gu
-from tests import kv4_ref as ref
+
 from tests.test_gpu_kv4 import BF16_WEIGHTS, _check_attention, _filled, _i32, _kv
 
 pytestmark = pytest.mark.gpu
@@ -343,3 +343,17 @@ def test_a_forked_and_compacted_pool():
     cache[:, pool.num_pages - pool.free_pages:] = 255          # what is free may hold anything
     assert all(torch.equal(x, y) for x, y in zip(before, reads(a, 40)))
     assert all(torch.equal(x, y) for x, y in zip(longer, reads(b, 70)))
+
+
+@pytest.mark.parametrize("new,hq,hk", STEPS)
+@pytest.mark.parametrize("scale", [-0.3, 0.0])
+def test_scales_below_and_at_zero(new, hq, hk, scale):
+    dim, lengths = 64, [100, 130, 80]
+    cache, table, own = _filled(np.random.default_rng(4), lengths, 16, hk, dim, 3)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q, lse = _queries(cu[-1], hq, dim), torch.empty(cu[-1], hq, device="cuda")
+    for ws in (_workspace(dim), None):
+        out = fp8mm.mxfp4_kv_attention(q.cuda(), cache.data.cuda(), _i32(table), _i32(lengths), 16, cu_seqlens=_i32(cu),
+                                       scale=scale, lse=lse, workspace=ws)
+        _check_attention(out, lse, q, cache, own, lengths, cu, scale,
+                         BF16_WEIGHTS if ws is not None and new[0] > 1 else 2.0 ** -10)
