@@ -18,9 +18,9 @@
 // guessed, and a captured graph follows the lengths in memory.
 // Bound by reading the cache, 17 D bytes per 16 tokens and head, once, and close
 // behind it by the conversions (two a clock and SM, 8 per record and lane of
-// each operand: the ALU pipe is 66 % busy).  Measured: 4 contexts of 100003 to
-// 131072 tokens, 32 heads on 8, 100 us, 77 % of the rate of a copy; 64 of 1 to
-// 8192 tokens 68 us, 64 %.  Measured on the way, the long contexts: eight warps
+// each operand: the ALU pipe is 63 % busy).  Measured: 4 contexts of 100003 to
+// 131072 tokens, 32 heads on 8, 100 to 109 us on different cards, 77 to 71 % of
+// the rate of a copy; 64 of 1 to 8192 tokens 68 us, 64 %.  Measured on the way, the long contexts: eight warps
 // of a CTA on one piece, joined through shared memory, 117 us; the same with a
 // warp that brings the records and one that joins results, 122 us (a CTA waits
 // for its slowest warp).
