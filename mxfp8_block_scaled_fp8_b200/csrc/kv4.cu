@@ -357,10 +357,10 @@ fp8mm_status qk_norm_rope(const void* q_bf16, int64_t q_stride_t, int64_t q_stri
   p.rot = static_cast<int32_t>(rot_dim);
   p.max_pos = static_cast<int32_t>(max_pos);
   p.eps = eps;
-  // warps of a token: one that walks all its heads, keeping the angles (8192
-  // tokens of 40 heads: 39.6 us, 42.9 with three); more, down to one step each,
-  // while the tokens alone would not fill the SMs
-  const int64_t steps = cdiv(q_heads + k_heads, 2 * (256 / head_dim));
+  // warps of a token: one that walks all its heads, keeping the angles, and more, down to one step each, while the
+  // tokens alone would not fill the SMs (8192 tokens of 40 heads, before the steps were joined: 39.6 us with one
+  // warp, 42.9 with three)
+  const int64_t step = kNormUnroll * (256 / head_dim), steps = cdiv(q_heads, step) + cdiv(k_heads, step);
   const int64_t fill = std::max<int64_t>(1, static_cast<int64_t>(dev.sms) * 32 / tokens);
   p.slices = static_cast<int32_t>(std::min(steps, fill));
   const int64_t blocks = cdiv(tokens * p.slices, kNormThreads / 32);

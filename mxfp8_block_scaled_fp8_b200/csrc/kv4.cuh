@@ -522,111 +522,127 @@ struct QkNormArgs {
   int32_t slices;  // warps per token
 };
 constexpr int kNormThreads = 128;
+constexpr int kNormUnroll = 4;
 
 // One warp per (token, slice of the heads); D / 8 lanes per head, so a warp
-// takes 256 / D heads at once.  The token's angles stay in registers while the
-// warp walks its heads, and the next heads' loads are in flight.  y = x *
-// rsqrt(mean x^2 + eps) * w in fp32, rotated in fp32, rounded once to bf16.
-// Bound by HBM for long prompts (each element read and written once; 8192
-// tokens of 40 heads of 128: 39.6 us, 4.3 TB/s, against 44.6 with a warp's
-// loads only behind its position), by latency for a decode step.
+// takes 256 / D heads side by side and kNormUnroll of these in a step, while the
+// next step's loads are in flight.  y = r (x_i w_i cos +- x_j w_j sin), r =
+// rsqrt(mean x^2 + eps): the weights join the token's angles once for all its
+// query heads and once for its key heads, and partners exchange bf16 pairs.
+// fp32 throughout, rounded once.  Bound by HBM for long prompts (each element
+// read and written once), by latency for a decode step (64 tokens 2.5 us).
+// 8192 tokens of 40 heads of 128: 34.3 us, 4.9 TB/s; steps of 2 heads 41.8, of 4
+// 37.0, of 16 42.0; weights and angles apart, fp32 partners 39.6.
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const QkNormArgs p) {
   constexpr int L = D / 8;         // lanes of a head
-  constexpr int HW = 32 / L;       // heads of a warp's step
-  constexpr int U = 2;             // steps whose loads are in flight together
+  constexpr int HW = 32 / L;       // heads that a warp takes side by side
+  constexpr int U = kNormUnroll;   // and of these, one after the other, in a step
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int l = lane % L, sub = lane / L;
+  const int l = lane % L, sub = lane / L, e0 = 8 * l;
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * (kNormThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = wid / p.slices;
   if (t >= p.tokens) return;
-  const int slice = static_cast<int>(wid - t * p.slices);
-  const int heads = p.q_heads + p.k_heads;
+  // steps of queries, then of keys
+  const int q_steps = (p.q_heads + HW * U - 1) / (HW * U), steps = q_steps + (p.k_heads + HW * U - 1) / (HW * U);
   uint4 v[U];
-  auto load = [&](int h0) {
+  auto load = [&](int s) {
+    const bool keys = s >= q_steps;
+    const __nv_bfloat16* x = (keys ? p.k + t * p.k_st : p.q + t * p.q_st) + e0;
+    const int64_t sh = keys ? p.k_sh : p.q_sh;
+    const int h0 = (keys ? s - q_steps : s) * (HW * U) + sub, heads = keys ? p.k_heads : p.q_heads;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * HW + sub;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (h < heads)
-        v[u] = ld_stream_16(h < p.q_heads ? p.q + t * p.q_st + h * p.q_sh + 8 * l
-                                          : p.k + t * p.k_st + (h - p.q_heads) * p.k_sh + 8 * l);
-    }
+    for (int u = 0; u < U; ++u) v[u] = h0 + u * HW < heads ? ld_stream_16(x + (h0 + u * HW) * sh) : make_uint4(0, 0, 0, 0);
   };
+  int s = static_cast<int>(wid - t * p.slices);
   const int pos = p.pos[t];
-  load(slice * HW * U);  // beside the position and the angles
-  if (pos < 0) return;   // a padding row
+  load(s);              // beside the position and the angles
+  if (pos < 0) return;  // a padding row
   if (pos >= p.max_pos) {
     if (lane == 0) record_index_error(kSitePosition);
     return;
   }
   const int half = p.rot / 2;
-  const int e0 = 8 * l;
-  const bool turned = e0 < p.rot;
-  const bool second = !kInterleaved && e0 >= half;
-  const int partner = kInterleaved ? lane : (turned ? (second ? lane - half / 8 : lane + half / 8) : lane);
-  float cs[8], sn[8];  // of elements e0 + i (interleaved: of pairs e0 / 2 + i, i < 4)
-  if (turned) {
-    const float* row = p.cos_sin + pos * p.cs_stride;
-    const int a0 = kInterleaved ? e0 / 2 : (second ? e0 - half : e0);
+  const bool turned = e0 < p.rot, second = !kInterleaved && e0 >= half;
+  // element e0 + i turns with element pe + i (interleaved: with its neighbour)
+  const int pe = kInterleaved || !turned ? e0 : (second ? e0 - half : e0 + half), partner = lane + (pe - e0) / 8;
+  // y_i = r (x_i a_i + x_partner b_i): the weights joined with the angles
+  float a[8], b[8];
+  auto factors = [&](const __nv_bfloat16* w) {
+    float c[8], d[8];
 #pragma unroll
-    for (int i = 0; i < (kInterleaved ? 4 : 8); i += 4) {
-      const float4 c = *reinterpret_cast<const float4*>(row + a0 + i);
-      const float4 d = *reinterpret_cast<const float4*>(row + half + a0 + i);
-      cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
-      sn[i] = d.x, sn[i + 1] = d.y, sn[i + 2] = d.z, sn[i + 3] = d.w;
+    for (int i = 0; i < 8; ++i) c[i] = 1.f, d[i] = 0.f;
+    if (turned) {
+      const float* row = p.cos_sin + pos * p.cs_stride + (kInterleaved ? e0 / 2 : (second ? pe : e0));
+#pragma unroll
+      for (int i = 0; i < (kInterleaved ? 4 : 8); i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(row + i), y = *reinterpret_cast<const float4*>(row + half + i);
+        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (kInterleaved) {
+            c[2 * k] = c[2 * k + 1] = xs[k];
+            d[2 * k] = -ys[k], d[2 * k + 1] = ys[k];
+          } else {
+            c[i + k] = xs[k], d[i + k] = second ? ys[k] : -ys[k];
+          }
+        }
+      }
     }
-  }
-  for (int h0 = slice * HW * U; h0 < heads; h0 += p.slices * HW * U) {
+    float wa[8], wb[8];
+    const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    bf16x8_to_f32(w != nullptr ? *reinterpret_cast<const uint4*>(w + e0) : ones, wa);
+    bf16x8_to_f32(w != nullptr ? *reinterpret_cast<const uint4*>(w + pe) : ones, wb);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = wa[i] * c[i];
+      b[i] = wb[kInterleaved ? i ^ 1 : i] * d[i];
+    }
+  };
+  for (int have = -1; s < steps; s += p.slices) {
     uint4 x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) x[u] = v[u];
-    load(h0 + p.slices * HW * U);
+    if (s + p.slices < steps) load(s + p.slices);
+    const int keys = s >= q_steps;
+    if (keys != have) {
+      factors(keys ? p.kw : p.qw);
+      have = keys;
+    }
+    __nv_bfloat16* out = (keys ? p.ko + t * p.ko_st : p.qo + t * p.qo_st) + e0;
+    const int64_t sh = keys ? p.ko_sh : p.qo_sh;
+    const int h0 = (keys ? s - q_steps : s) * (HW * U) + sub, heads = keys ? p.k_heads : p.q_heads;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * HW + sub;
-      const bool is_q = h < p.q_heads;
-      float f[8];
+      float f[8], o[8];
       bf16x8_to_f32(x[u], f);
+      float r = 1.f;
       if (p.qw != nullptr) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        float w[8];
-        bf16x8_to_f32(*reinterpret_cast<const uint4*>((is_q ? p.qw : p.kw) + e0), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+        for (int k = 1; k < L; k <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, k);
+        r = rsqrtf(ss * (1.f / D) + p.eps);
       }
-      float y[8];
       if constexpr (kInterleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[2 * i] = turned ? f[2 * i] * cs[i] - f[2 * i + 1] * sn[i] : f[2 * i];
-          y[2 * i + 1] = turned ? f[2 * i + 1] * cs[i] + f[2 * i] * sn[i] : f[2 * i + 1];
-        }
+        for (int i = 0; i < 8; ++i) o[i] = f[i ^ 1];
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(0xFFFFFFFFu, f[i], partner);
-          y[i] = turned ? f[i] * cs[i] + (second ? o : -o) * sn[i] : f[i];
-        }
+        const uint4 y = make_uint4(__shfl_sync(0xFFFFFFFFu, x[u].x, partner), __shfl_sync(0xFFFFFFFFu, x[u].y, partner),
+                                   __shfl_sync(0xFFFFFFFFu, x[u].z, partner), __shfl_sync(0xFFFFFFFFu, x[u].w, partner));
+        bf16x8_to_f32(y, o);
       }
-      if (h < heads) {
-        uint32_t o[4];
+      uint32_t y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-          o[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        __nv_bfloat16* dst = is_q ? p.qo + t * p.qo_st + h * p.qo_sh + e0
-                                  : p.ko + t * p.ko_st + (h - p.q_heads) * p.ko_sh + e0;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(fmaf(f[2 * i], a[2 * i], o[2 * i] * b[2 * i]) * r,
+                                                       fmaf(f[2 * i + 1], a[2 * i + 1], o[2 * i + 1] * b[2 * i + 1]) * r);
+        y[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
+      if (h0 + u * HW < heads) *reinterpret_cast<uint4*>(out + (h0 + u * HW) * sh) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
 }
