@@ -410,7 +410,7 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
  * attend).  A row that sees no token (seq_lens[s] == 0, or a position below 0) gives zeros.  Scores, softmax
  * statistics and sums are fp32; queries enter exactly, weights with 11 bits, or 8 in a call with a workspace and
  * 96 or more rows of a key/value head per sequence (rows / batch, rounded up, times g), whose products are
- * bf16.  Rows of a sequence with a page id outside the pool are unspecified.
+ * bf16 (values past 2^100 may overflow there).  Rows of a sequence with a page id outside the pool are unspecified.
  *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned
  *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
  *        empty row

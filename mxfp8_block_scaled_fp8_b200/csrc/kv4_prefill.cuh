@@ -7,8 +7,8 @@
 //   P = 2^(S scale log2 e - m), bf16, written over S
 //   O += P V        P from TMEM, V^T bf16 in shared memory, fp32 in TMEM
 // Codes become bf16 exactly (a code has two significant bits, the exponent is
-// bf16's), so keys and values enter without error and without a range limit;
-// weights are rounded to 8 bits, and the row's sum is of the fp32 weights.
+// bf16's), so keys and values enter without error; weights are rounded to 8
+// bits, and the row's sum is of the fp32 weights.
 //
 // Warps: 0-3 and 4-7 the softmax of the two halves (a thread per row), 8-10
 // bring keys and 11-13 values and write them as bf16 tiles, 14 and 15 issue the
@@ -556,9 +556,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           const int left = vis - (k0 + static_cast<int>(it - it0)) * kPreTokens;  // tokens of the step that the row sees
           const bool masked = __any_sync(0xFFFFFFFFu, left < kPreTokens);
           // The maximum only keeps weights and sums in fp32's range (a bf16
-          // weight has 8 bits at any size), so a step is not searched for it:
-          // the rows' first sets it, and one whose weights sum to more than
-          // 2^40 is taken again with a new one.
+          // weight has 8 bits at any size), so a step is not searched for it: the
+          // rows' first sets it, and one whose weights sum to more than 2^16 is
+          // taken again with a new one (values up to 2^100 stay in range).
           bool search = __any_sync(0xFFFFFFFFu, it == it0 || (m == -INFINITY && left > 0));
           uint32_t w[32];
           while (true) {
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
               w[e] = *reinterpret_cast<const uint32_t*>(&v);
             }
             const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            if (!search && __any_sync(0xFFFFFFFFu, !(all <= 0x1p40f))) {
+            if (!search && __any_sync(0xFFFFFFFFu, !(all <= 0x1p16f))) {
               search = true;
               continue;
             }

@@ -287,10 +287,11 @@ def test_strided_results(new, hq, hk):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 96])
 @pytest.mark.parametrize("low,high", [(-50.0, 50.0), (50.0, -50.0), (0.0, 0.0)])
-def test_scores_that_rise_along_a_prompt(dim, low, high):
+def test_scores_that_rise_along_a_prompt(dim, low, high, size):
     """Scores from `low` to `high` (natural units) along 700 tokens: rows whose first tokens' maximum is far below
-    the last's, and far above."""
+    the last's, and far above; values of any size."""
     n, rows, heads = 700, 130, 2
 
     def make(length, h, d, seed):
@@ -298,7 +299,7 @@ def test_scores_that_rise_along_a_prompt(dim, low, high):
         ramp = torch.linspace(low, high, length)[:, None, None]
         k = 0.02 * k
         k[..., :32] = (ramp / 32).expand(length, h, 32).bfloat16()
-        return k, v
+        return k, v * size
 
     cache, table, own = _filled(np.random.default_rng(3), [n], 64, 1, dim, 9, make)
     q = _queries(rows, heads, dim)
