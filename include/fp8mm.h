@@ -408,9 +408,11 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
  *   out[r, h] = sum_j softmax_j(scale <q[r, h], k[j, h / g]>) v[j, h / g],  j <= position of row r,
  * g = q_heads / kv_heads, row i of sequence s's n rows at position seq_lens[s] - n + i (append first, then
  * attend).  A row that sees no token (seq_lens[s] == 0, or a position below 0) gives zeros.  Scores, softmax
- * statistics and sums are fp32; queries enter exactly, weights with 11 bits, or 8 in a call with a workspace and
- * 96 or more rows of a key/value head per sequence (rows / batch, rounded up, times g), whose products are
- * bf16 (values past 2^100 may overflow there).  Rows of a sequence with a page id outside the pool are unspecified.
+ * statistics and sums are fp32.  Queries enter as f16, scaled row by row so that their 8 bits are kept down to 2^-27
+ * of the row's largest magnitude, and weights with 11 bits; but in a call with a workspace and 96 or more rows of a
+ * key/value head per sequence (rows / batch, rounded up, times g) queries enter exactly and weights with 8 bits, and
+ * products are bf16 (values past 2^100 may overflow there).  Which of the two a row gets goes by its call.  Rows of a
+ * sequence with a page id outside the pool are unspecified.
  *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned
  *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
  *        empty row

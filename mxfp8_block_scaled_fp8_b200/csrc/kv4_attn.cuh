@@ -301,7 +301,7 @@ struct AttnWarp {
         float f[8];
         bf16x8_to_f32(v[t][b], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= f0 * f1;
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * f0 * f1;  // one after the other: f0 f1 may be 2^140
         to.frag[t][b][lane] = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
       }
       // key exponents count one up: one factor 2 to take back

@@ -1,0 +1,103 @@
+"""Magnitudes and values at the ends of their types in the cache operators:
+queries of any finite size, values that only some of a tile's rows see,
+infinities and NaN, scales of any size.
+
+Tolerances.  What tests/test_gpu_kv4.py derives, by row: an element is off by
+2^-8 of itself (bf16), by the weights' rounding (2^-10 of the sum of weight *
+|v|, or bf16's 2^-8 + 2^-11 on the kernel for many rows), and by what lies below
+f16's normal range: by 2^-25 * |code| a token, |code| <= 6, where a block's sums
+are 1 and more (or the reference is within 2^8 of what the row needs, which is as
+good): n tokens are off by n * 6 * 2^-25 of the block's largest |sum|, and that sum
+is at most the sum of weight * (largest |v| of the block): n * 2^-22 of that.  Nothing counts that the row does not see."""
+import math
+
+import pytest
+import torch
+
+import mxfp8_block_scaled_fp8_b200 as fp8mm
+from tests import gpu_util as gu
+from tests import kv4_ref as ref
+from tests.test_gpu_kv4 import BF16_WEIGHTS, MANY_ROWS, _i32, _kv
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    gu.require_gpu()
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert fp8mm.last_device_error() == 0
+
+
+def _workspace(dim):
+    return torch.zeros(fp8mm.mxfp4_kv_attention_workspace_bytes(dim), dtype=torch.uint8, device="cuda")
+
+
+def _written(k, v, page_size=16):
+    """One sequence's tokens appended: (cache, page table, length), and the stored fp64 keys and values."""
+    n, heads, dim = k.shape
+    pages = -(-n // page_size)
+    table = _i32([torch.randperm(pages, generator=torch.Generator().manual_seed(n)).tolist()])
+    cache = torch.full((pages, fp8mm.mxfp4_kv_page_bytes(page_size, heads, dim)), 255, dtype=torch.uint8, device="cuda")
+    fp8mm.mxfp4_kv_append(k.cuda(), v.cuda(), cache, table, _i32([n]), page_size, cu_seqlens=_i32([0, n]))
+    stored = []
+    for x in (k, v):
+        finite = torch.isfinite(x.float()).unflatten(-1, (-1, 32)).all(-1).repeat_interleave(32, -1)
+        stored.append(torch.where(finite, ref.value(*ref.quantize(torch.where(finite, x, 0))), math.nan))
+    return cache, table, stored
+
+
+def _run(q, written, heads, scale, workspace, page_size=16):
+    cache, table, (k, _) = written
+    lse = torch.full(q.shape[:2], 5.0, device="cuda")
+    out = fp8mm.mxfp4_kv_attention(q.cuda(), cache, table, _i32([k.shape[0]]), page_size, cu_seqlens=_i32([0, q.shape[0]]),
+                                   scale=scale, lse=lse, workspace=workspace)
+    return out.double().cpu(), lse.double().cpu()
+
+
+def _check_row(out, lse, q, k, v, scale, weights):
+    """One row of one head, q [dim], over the keys and values [n, dim] that it sees."""
+    s = k @ q.double() * scale
+    p = torch.softmax(s, 0)
+    want, mag = p @ v, p @ v.abs()
+    peak = (p[:, None] * v.unflatten(-1, (-1, 32)).abs().amax(-1)).sum(0).repeat_interleave(32)
+    lim = 2.0 ** -8 * want.abs() + weights * mag + k.shape[0] * 2.0 ** -22 * peak + 1e-37
+    bad = (out - want).abs() / lim
+    assert torch.isfinite(out).all() and bad.max() <= 1, (bad.max(), want[bad.argmax()], out[bad.argmax()])
+    wlse = torch.logsumexp(s, 0)
+    assert (lse - wlse).abs() <= 2.0 ** -14 * (1 + wlse.abs()), (lse, wlse)
+
+
+def _kinds(rows, group, dim):
+    """(workspace, weights) of the calls that a test makes: cut or not, and which kernel the rows take."""
+    many = rows * group >= MANY_ROWS
+    return ((_workspace(dim), BF16_WEIGHTS if many else 2.0 ** -10), (None, 2.0 ** -10))
+
+
+def _check_queries(dim, rows, sizes):
+    """Rows whose largest magnitude is sizes[h] in query head h, zeros among them, three heads on each of two."""
+    n, heads = 150, 2
+    written = _written(*_kv(n, heads, dim, 4))
+    g = torch.Generator().manual_seed(rows)
+    q = torch.randn(rows, heads, 3, dim, generator=g)
+    q = q / q.abs().amax(-1, keepdim=True) * torch.tensor(sizes).view(heads, 3, 1)
+    q[..., ::7] = 0
+    q = q.flatten(1, 2).bfloat16()
+    assert (q.abs().amax(-1) > 0).all()
+    for ws, weights in _kinds(rows, 3, dim):
+        out, lse = _run(q, written, heads, dim ** -0.5, ws)
+        for i in range(rows):
+            for h in range(6):
+                k, v = (x[:n - rows + i + 1, h // 3] for x in written[2])
+                _check_row(out[i, h], lse[i, h], q[i, h], k, v, dim ** -0.5, weights)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_queries_of_tiny_size(dim, rows):
+    """Down to bf16's smallest subnormal, beside rows of ordinary size."""
+    _check_queries(dim, rows, (2.0 ** -113, 2.0 ** -114, 2.0 ** -126, 2.0 ** -133, 1.0, 2.0 ** -120))
