@@ -224,6 +224,9 @@ struct AttnCutting {
 
 constexpr float kSlack = 2.f;  // how far (log2) a score may pass the running maximum before that moves
 constexpr float kHead = 2.f;   // to so far above it
+// Scores (log2) from this size on are taken one by one (step_slow): a fused x sc - m has the exact product, m a rounded
+// one, and the difference, half an ulp of the score, is below 2^-12 only under it.
+constexpr float kExact = 4096.f;
 constexpr int kSpare = 8;      // how far E_b may be above what the weights need, to take in the step's exponents
 constexpr int kMinRef = 13;    // so that 2^(127 + kBias - E_b) is finite
 constexpr int kBias = 12;      // weights enter the second product times 2^kBias: 2^(kSlack + 1 + kBias) < 2^16
@@ -244,7 +247,7 @@ struct AttnWarp {
   using Query = AttnQuery<D, NT, FOLD>;
   float o[NT][NJ][4];          // O^T: rows d = 16 j + g (+ 8), columns 2 c (+ 1)
   float sc[NT][2], m[NT][2], l[NT][2];  // of columns 2 c, 2 c + 1
-  float limit[NT][2];          // (m + kSlack) / sc: raw scores above it move the maximum
+  float limit[NT][2];          // (m + kSlack) / sc: raw scores above it move the maximum; -inf: all go the slow way
   float unit[NB];              // 2^(127 + kBias - E_b), which tells E_b (kMinRef and up)
   uint32_t ref_half;           // E_b / 2 in bytes, with the bytes' top bits set
   int vis[NT][2];              // tokens visible to columns 2 c, 2 c + 1; INT_MAX where the column is no row
@@ -503,7 +506,7 @@ struct AttnWarp {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float& y = x[u][t][k + 2 * h];
-            y = end[u][h] >= seen ? -INFINITY : y * sc[t][k];
+            y = end[u][h] >= seen ? -INFINITY : __fmul_rn(y, sc[t][k]);
             mx = fmaxf(mx, y);
           }
 #pragma unroll
@@ -514,7 +517,7 @@ struct AttnWarp {
         // a column that is no row, or has met nothing yet, holds no sum that the references must keep
         if (row && m[t][k] != -INFINITY) drop = min(drop, same ? 0 : static_cast<int>(fminf(mn - m[t][k], 1000.f)));
         m[t][k] = mn;
-        limit[t][k] = sc[t][k] > 0.f ? (mn + kSlack) / sc[t][k] : (mn == -INFINITY ? -INFINITY : INFINITY);
+        limit[t][k] = fabsf(mn) >= kExact ? -INFINITY : (sc[t][k] > 0.f ? (mn + kSlack) / sc[t][k] : INFINITY);
         const float at = mn == -INFINITY ? 0.f : mn;
         l[t][k] *= r[t][k];
 #pragma unroll

@@ -48,6 +48,10 @@ constexpr int kPreStages = 4;        // steps whose keys, and whose values, have
 constexpr int kPreThreads = 512;
 constexpr int kPreKeyWarps = 3, kPreValueWarps = 3;  // that write key and value tiles
 constexpr float kPreSlack = 8.f;
+// A fused s sc - m has the exact product, m a rounded one: from this size of m (log2) on they may be 1 and more apart, up or
+// down.  Such a row's weights are 2^((s - base) sc), base its largest raw score, and its m stands at -inf, so that every
+// step is searched (pre_search).
+constexpr float kPreExact = 16777216.f;
 // What a tile costs beside its tokens, in units of 64 tokens (queries to shared
 // memory, the chain's fill and drain, the rows' store): 644 us with 6, 618 with
 // 8, 619 with 11.
@@ -282,6 +286,7 @@ struct PreShared {
   PrePiece piece[kPreThreads / 32];  // of each warp: they go from piece to piece on their own
   uint64_t full[2][kPreStages], empty[2][kPreStages];  // of keys, of values
   uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], drain;
+  float base[kPreRows];  // PreRow::base
   uint32_t tmem;
   int abort;
 };
@@ -377,6 +382,69 @@ struct PreValues {
     }
   }
 };
+
+// What a softmax thread keeps of its row.
+struct PreRow {
+  float m, l;  // the maximum that the weights are taken under, the sum of weights
+  float base;  // the largest raw score, of a row past kPreExact; else -inf
+  bool ok;     // no wait has expired
+};
+// A step's scores at buf searched for the row's maximum, `left` of them to be seen; where it moves, the sums at o_addr are
+// scaled, after the products of the step before have landed (`done`; nullptr: there are none).  Not inlined: in the loop it
+// takes registers from the steps that are not searched (641 us instead of 618, by the place of its branch).
+template <int D>
+__device__ __noinline__ PreRow pre_search(PreRow r, uint32_t buf, uint32_t o_addr, int left, float sc, uint64_t* done,
+                                          uint32_t parity, uint64_t timeout, volatile int* abort) {
+  float raw = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 64; i += 32) {
+    uint32_t s[32];
+    tmem_load_32(buf + i, s);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (i + e < left) raw = fmaxf(raw, __uint_as_float(s[e]));
+  }
+  const float mx = raw * sc;
+  float f = 1.f;
+  if (r.base != -INFINITY) {
+    if (raw > r.base) {
+      f = ex2((r.base - raw) * sc);
+      r.base = raw;
+    }
+  } else if (mx > r.m + kPreSlack || (r.m == -INFINITY && mx != -INFINITY)) {
+    f = ex2(r.m - mx);
+    r.m = mx;
+    if (fabsf(r.m) >= kPreExact) r.base = raw, r.m = -INFINITY;
+  }
+  r.l *= f;
+  if (__any_sync(0xFFFFFFFFu, f != 1.f) && done != nullptr) {
+    r.ok = warp_wait(done, parity, timeout, abort, kSiteEpiSync);
+    if (!r.ok) return r;
+    tc_fence_after();
+#pragma unroll 1
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t o[16];
+      tmem_load_16(o_addr + 16 * i, o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+      tmem_st_32x32b_x16(o_addr + 16 * i, o);
+    }
+    tmem_st_wait();
+  }
+  if (__any_sync(0xFFFFFFFFu, r.base != -INFINITY)) {  // the differences take the scores' place
+#pragma unroll 1
+    for (int i = 0; i < 64; i += 16) {
+      uint32_t s[16];
+      tmem_load_16(buf + i, s);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (r.base != -INFINITY) s[e] = __float_as_uint(__uint_as_float(s[e]) - r.base);
+      tmem_st_32x32b_x16(buf + i, s);
+    }
+    tmem_st_wait();
+  }
+  return r;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAttnArgs p) {
@@ -546,6 +614,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
         const int vis = rho < rows ? min(len, max(len - n + rho / p.group + 1, 0)) : 0;
         const float sc = fabsf(p.scale_log2);
         float m = -INFINITY, l = 0.f;
+        sh.base[threadIdx.x] = -INFINITY;
         bool ok = true;
         const uint32_t it0 = tile0, it1 = tile0 + (k1 - k0);
         for (uint32_t it = it0; it < it1; ++it) {
@@ -561,43 +630,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           // taken again with a new one (values up to 2^100 stay in range).
           bool search = __any_sync(0xFFFFFFFFu, it == it0 || (m == -INFINITY && left > 0));
           uint32_t w[32];
-          while (true) {
+          for (bool searched = false;;) {
+            if (search) {
+              const PreRow row = pre_search<D>({m, l, sh.base[threadIdx.x], true}, buf, o_addr, left, sc,
+                                               it != it0 ? &sh.pv_done[t][(it - 1) & 1] : nullptr, ((it - 1) >> 1) & 1,
+                                               timeout, abort);
+              m = row.m, l = row.l, sh.base[threadIdx.x] = row.base, ok = row.ok;
+              if (!ok) break;
+              searched = true;
+            }
             uint32_t s[64];
             tmem_load_64(buf, s);
             if (masked) {
 #pragma unroll
               for (int e = 0; e < 64; ++e)
                 if (e >= left) s[e] = 0xFF800000u;
-            }
-            if (search) {
-              float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
-#pragma unroll
-              for (int e = 2; e < 64; e += 2) {
-                a = fmaxf(a, __uint_as_float(s[e]));
-                b = fmaxf(b, __uint_as_float(s[e + 1]));
-              }
-              const float mx = fmaxf(a, b) * sc;
-              float f = 1.f;
-              if (mx > m + kPreSlack || (m == -INFINITY && mx != -INFINITY)) {
-                f = ex2(m - mx);
-                m = mx;
-                l *= f;
-              }
-              if (__any_sync(0xFFFFFFFFu, f != 1.f) && it != it0) {
-                // scale what is summed; the products of the step before have landed first
-                ok = warp_wait(&sh.pv_done[t][(it - 1) & 1], ((it - 1) >> 1) & 1, timeout, abort, kSiteEpiSync);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int i = 0; i < D / 16; ++i) {
-                  uint32_t o[16];
-                  tmem_load_16(o_addr + 16 * i, o);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st_32x32b_x16(o_addr + 16 * i, o);
-                }
-                tmem_st_wait();
-              }
             }
             const float at = m == -INFINITY ? 0.f : m;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -611,10 +658,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
               w[e] = *reinterpret_cast<const uint32_t*>(&v);
             }
             const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            if (!search && __any_sync(0xFFFFFFFFu, !(all <= 0x1p16f))) {
-              search = true;
-              continue;
-            }
+            search = !searched && __any_sync(0xFFFFFFFFu, !(all <= 0x1p16f));
+            if (search) continue;
             l += all;
             break;
           }
@@ -639,6 +684,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           __syncwarp();
           if (pc.k0 < pc.k1) queries(t);
         }
+        if (sh.base[threadIdx.x] != -INFINITY) m = sh.base[threadIdx.x] * sc;
         // ---- the rows, or the piece's partial result
         if (ok && k0 < k1) ok = warp_wait(&sh.pv_done[t][(it1 - 1) & 1], ((it1 - 1) >> 1) & 1, timeout, abort, kSiteEpiSync);
         if (ok) {

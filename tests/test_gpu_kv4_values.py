@@ -101,3 +101,37 @@ def _check_queries(dim, rows, sizes):
 def test_queries_of_tiny_size(dim, rows):
     """Down to bf16's smallest subnormal, beside rows of ordinary size."""
     _check_queries(dim, rows, (2.0 ** -113, 2.0 ** -114, 2.0 ** -126, 2.0 ** -133, 1.0, 2.0 ** -120))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_queries_of_huge_size(dim, rows):
+    """The largest score takes all of the weight, whatever its rounding in fp32."""
+    _check_queries(dim, rows, (2.0 ** 20, 2.0 ** 30, 2.0 ** 60, 2.0 ** 100, 1.0, 2.0 ** 110))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [1, 4, 40])
+@pytest.mark.parametrize("step", [2.0 ** 20, 2.0 ** 26, 2.0 ** 40])
+def test_scores_past_the_precision_of_fp32(dim, rows, step):
+    """Scores of up to 120 steps whose rounding in fp32 is larger than one: tokens share the largest, in the first
+    step, the last and between, and the softmax is theirs alone."""
+    n, heads = 260, 1
+    k = torch.zeros(n, heads, dim)
+    k[:, :, 0] = (torch.arange(n) % 97).clamp(max=96)[:, None] // 24
+    top = [30, 31, 140, n - rows]
+    k[top, :, 0] = 6.0
+    k[:, :, 1] = 0.5
+    _, v = _kv(n, heads, dim, 8)
+    written = _written(k.bfloat16(), v)
+    assert torch.equal(written[2][0], k.double())
+    q = torch.zeros(rows, 3, dim)
+    q[..., 0] = torch.tensor([1.0, 1.2109375, 1.7578125]) * step
+    q[..., 1] = 3.0 * step
+    q = q.bfloat16()
+    for ws, weights in _kinds(rows, 3, dim):
+        out, lse = _run(q, written, heads, 0.7, ws)
+        for i in range(rows):
+            for h in range(3):
+                kk, vv = (x[:n - rows + i + 1, 0] for x in written[2])
+                _check_row(out[i, h], lse[i, h], q[i, h], kk, vv, 0.7, weights)
