@@ -43,6 +43,12 @@
 // reference, fewer down to 2^-36.  E_b follows the largest weight * 2^e that
 // the tile's rows have met, as the softmax's maximum follows the largest
 // score, so a token of no weight does not raise it, however large its values.
+// The rows of a tile share it.  A row whose sums come out small in its units
+// (kLow), since another row has met values far above what this one has, is taken
+// again by itself with its own: a token with huge values, seen by some of the
+// rows, leaves the others their bits.  (64 sequences of 1 to 8192 tokens 65.6 us in
+// a graph, 64.8 without that look at the sums; references by row, which cost
+// multiplications and registers in every step, 69 to 73 us.)
 #pragma once
 
 #include <climits>
@@ -229,6 +235,10 @@ constexpr float kHead = 2.f;   // to so far above it
 constexpr float kExact = 4096.f;
 constexpr int kSpare = 8;      // how far E_b may be above what the weights need, to take in the step's exponents
 constexpr int kMinRef = 13;    // so that 2^(127 + kBias - E_b) is finite
+// A row's sums below this, in the units that its weights were rounded in, are not to be had from shared references: each
+// token is off by 6 * 2^-25 at most where its weight is below f16's normal range (weights of the row's largest score alone
+// give 2^(kBias - kHead) * |code| * 2^(e - E_b)).
+constexpr float kLow = 1.f;
 constexpr int kBias = 12;      // weights enter the second product times 2^kBias: 2^(kSlack + 1 + kBias) < 2^16
 
 // A tile's queries in shared memory, the same for all warps: fragments of the
@@ -312,9 +322,9 @@ struct AttnWarp {
     }
   }
 
-  __device__ __forceinline__ void begin(const KvAttnArgs& p, const AttnSeq& q, int row0, const Query& from) {
+  // active: bit i where row i of the tile is worked on.
+  __device__ __forceinline__ void begin(const KvAttnArgs& p, const AttnSeq& q, int row0, const Query& from, uint32_t active) {
     const int c = threadIdx.x & 3;
-    const int rows = min(q.n * p.group - row0, R);
     const int at = row0 / p.group, off = row0 - at * p.group;
     const int seen = q.len - q.n + at + 1;  // tokens visible to the tile's first row
 #pragma unroll
@@ -325,7 +335,7 @@ struct AttnWarp {
         sc[t][k] = from.factor[row];
         m[t][k] = limit[t][k] = -INFINITY;
         l[t][k] = 0.f;
-        vis[t][k] = row < rows ? seen + (off + row) / p.group : INT_MAX;
+        vis[t][k] = (active >> row) & 1u ? seen + (off + row) / p.group : INT_MAX;
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
@@ -577,10 +587,13 @@ struct AttnWarp {
 
   // Sums in real units, maxima and sums of weights of the columns; the two
   // folds joined (then columns 2 c, 2 c + 1 of the lanes with c < 2 count).
-  __device__ __forceinline__ void finish() {
+  // Returns the rows, of several active ones, whose sums in a block are below kLow.
+  __device__ __forceinline__ uint32_t finish(uint32_t active) {
+    uint32_t low = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float own[2] = {1.f, 1.f}, other[2] = {0.f, 0.f};
+      bool under[2] = {false, false};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -595,14 +608,32 @@ struct AttnWarp {
         }
       }
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int b = 0; b < NB; ++b) {
+        float top[2] = {0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float& y = o[t][j][k];
-          y = scale2(y, ref(j / 2) - 127 - kBias);
-          if constexpr (FOLD == 2) y = y * own[k & 1] + __shfl_xor_sync(0xFFFFFFFFu, y, 2) * other[k & 1];
+        for (int j = 2 * b; j < 2 * b + 2; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float& y = o[t][j][k];
+            if constexpr (FOLD == 2) y = y * own[k & 1] + __shfl_xor_sync(0xFFFFFFFFu, y, 2) * other[k & 1];
+            top[k & 1] = fmaxf(top[k & 1], fabsf(y));
+            y = scale2(y, ref(b) - 127 - kBias);
+          }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // (a block of zeros leaves E_b where it began)
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], off));
+          under[k] |= top[k] < kLow && ref(b) > kMinRef;
         }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, under[k] && l[t][k] > 0.f);  // lane c of a column 8 t + 2 c + k
+#pragma unroll
+        for (int c = 0; c < (FOLD == 2 ? 2 : 4); ++c) low |= ((who >> c) & 1u) << (8 * t + 2 * c + k);
+      }
     }
+    return (active & (active - 1)) != 0 ? low & active : 0;
   }
   // After finish(): f(row, d, value) for this lane's elements.
   template <typename F>
@@ -674,6 +705,12 @@ __device__ __forceinline__ void attn_job(const KvAttnArgs& p, const AttnPlan& pl
   attn_piece<R>(p, pc);
 }
 
+// The rows of the piece's tile, a bit each.
+template <int R>
+__device__ __forceinline__ uint32_t attn_rows(const KvAttnArgs& p, const AttnPiece& pc) {
+  return (1u << min(pc.q.n * p.group - pc.row0, R)) - 1;
+}
+
 // Output row `rho` of a tile's sequence and head.
 template <int D>
 __device__ __forceinline__ void attn_store(const KvAttnArgs& p, int lo, int rho, int head, int d4,
@@ -689,10 +726,10 @@ __device__ __forceinline__ void attn_store(const KvAttnArgs& p, int lo, int rho,
     p.lse[(lo + i) * p.lse_st + h] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// The rows of a tile that one warp has done alone.
+// The rows `done` of a tile that one warp has done alone.
 template <int D, int NT, int FOLD>
-__device__ __forceinline__ void attn_store_warp(const KvAttnArgs& p, const AttnPiece& pc, const AttnWarp<D, NT, FOLD>& w) {
-  const int rows = pc.q.n * p.group;
+__device__ __forceinline__ void attn_store_warp(const KvAttnArgs& p, const AttnPiece& pc, const AttnWarp<D, NT, FOLD>& w,
+                                                uint32_t done) {
   float inv[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -700,7 +737,7 @@ __device__ __forceinline__ void attn_store_warp(const KvAttnArgs& p, const AttnP
     for (int k = 0; k < 2; ++k) inv[t][k] = w.l[t][k] > 0.f ? 1.f / w.l[t][k] : 0.f;
   w.elements([&](int t, int k, int row, int d, float v) {
     const int rho = pc.row0 + row;
-    if (rho >= rows) return;
+    if (((done >> row) & 1u) == 0) return;
     const int i = rho / p.group;
     const int h = pc.head * p.group + (rho - i * p.group);
     p.out[static_cast<int64_t>(pc.q.lo + i) * p.o_st + h * p.o_sh + d] = __float2bfloat16_rn(v * inv[t][k]);
@@ -818,6 +855,7 @@ struct __align__(128) AttnShared {
   uint8_t ring[AttnCfg<D, NT, FOLD>::kRingBytes];
   AttnQuery<D, NT, FOLD> query;
   AttnPiece piece;
+  uint32_t active, low;  // rows of the piece that are worked on; that are to be taken again
   uint64_t full[kAttnStages];
 };
 
@@ -902,6 +940,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kAttnCtas : 1) kv4_att
   AttnPiece& pc = sh.piece;
   bool dead = false;  // a wait expired
   if (lane == 0) attn_job<R>(p, plan, per, cut, job, pc);
+  if (lane == 0) sh.active = attn_rows<R>(p, pc), sh.low = 0;
   __syncwarp();
   while (true) {
     {
@@ -911,7 +950,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kAttnCtas : 1) kv4_att
       w.put_queries(p, raw, sh.query);
     }
     __syncwarp();
-    w.begin(p, pc.q, pc.row0, sh.query);
+    w.begin(p, pc.q, pc.row0, sh.query, sh.active);
     const int len = pc.q.len, seq = pc.s, head = pc.head;
     while (ring.taken < ring.steps) {
       const int st = ring.taken % S;
@@ -934,29 +973,38 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kAttnCtas : 1) kv4_att
     }
     if (dead) break;
     // the tile's rows, or the piece's partial result
-    w.finish();
-    if (pc.u == pc.i0 && pc.end == pc.i1) {
-      attn_store_warp<D, NT, FOLD>(p, pc, w);
+    const uint32_t active = sh.active, low = w.finish(active), done = active & ~low;
+    const bool whole = pc.u == pc.i0 && pc.end == pc.i1, begins = pc.i0 >= pc.job_u;
+    if (whole) {
+      attn_store_warp<D, NT, FOLD>(p, pc, w, done);
     } else {
-      const bool begins = pc.i0 >= pc.job_u;
       float* part = p.partials + (2 * pc.job + (begins ? 1 : 0)) * static_cast<int64_t>(Cfg::kPartFloats);
       w.elements([&](int t, int k, int row, int d, float v) {
+        if (((done >> row) & 1u) == 0) return;
         part[row * D + d] = v;
         if (d == 0) {
           part[R * D + row] = w.m[t][k];
           part[R * D + R + row] = w.l[t][k];
         }
       });
-      if (begins && lane == 0)  // to the list of cut tiles
-        p.cuts[atomicAdd(&p.counters->cut, 1u)] =
-            AttnCut{static_cast<int>(pc.job), static_cast<int>(cut.job_of(pc.i1 - 1)), pc.q.lo, pc.head, pc.row0,
-                    min(pc.q.n * p.group - pc.row0, R)};
     }
+    const uint32_t more = sh.low | low;  // rows to take again, one by one
+    __syncwarp();
+    if (more != 0) {
+      if (lane == 0) sh.active = more & (0u - more), sh.low = more & (more - 1);
+      __syncwarp();
+      continue;
+    }
+    if (!whole && begins && lane == 0)  // to the list of cut tiles
+      p.cuts[atomicAdd(&p.counters->cut, 1u)] =
+          AttnCut{static_cast<int>(pc.job), static_cast<int>(cut.job_of(pc.i1 - 1)), pc.q.lo, pc.head, pc.row0,
+                  min(pc.q.n * p.group - pc.row0, R)};
     if (pc.end >= pc.job_end) break;
     __syncwarp();
     if (lane == 0) {
       pc.u = pc.end;
       attn_piece<R>(p, pc);
+      sh.active = attn_rows<R>(p, pc);
     }
     __syncwarp();
   }

@@ -135,3 +135,29 @@ def test_scores_past_the_precision_of_fp32(dim, rows, step):
             for h in range(3):
                 kk, vv = (x[:n - rows + i + 1, 0] for x in written[2])
                 _check_row(out[i, h], lse[i, h], q[i, h], kk, vv, 0.7, weights)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 30, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("rows,group", [(2, 2), (4, 2), (5, 3), (40, 3)])
+def test_outlier_values_that_other_rows_see(dim, size, rows, group):
+    """The last token's values, which only the last row sees, and those of a token that only the first query head of
+    each key/value head attends to, are 2^30 and more times the others': every row keeps its own precision."""
+    n, heads, at = 130, 2, 77
+    k, v = _kv(n, heads, dim, 6)
+    k, v = 0.02 * k.float(), v.float()
+    k[..., :32] = 0
+    k[at, :, :32] = 6.0
+    v[at, :, ::3] *= size
+    v[n - 1] *= size
+    written = _written(k.bfloat16(), v.bfloat16())
+    q = torch.randn(rows, heads, group, dim, generator=torch.Generator().manual_seed(2))
+    q[..., :32] = -1.0
+    q[:, :, 0, :32] = 1.0
+    q = q.flatten(1, 2).bfloat16()
+    for ws, weights in _kinds(rows, group, dim):
+        out, lse = _run(q, written, heads, 1.0, ws)
+        for i in range(rows):
+            for h in range(heads * group):
+                kk, vv = (x[:n - rows + i + 1, h // group] for x in written[2])
+                _check_row(out[i, h], lse[i, h], q[i, h], kk, vv, 1.0, weights)
