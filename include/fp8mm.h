@@ -362,7 +362,8 @@ fp8mm_status qk_norm_rope(const void* q_bf16, int64_t q_stride_t, int64_t q_stri
 /* A layer's key/value cache in pages, and the page table of a batch.
  * Keys and values are MXFP4: E2M1 codes, one UE8M0 exponent e per 32 elements of the head dimension, value =
  * code * 2^(e - 127), 4.25 bits per element.  e is the smallest with 6 * 2^(e - 127) >= the block's largest
- * magnitude (0 for a block of zeros): mxfp8_quantize's rule with E2M1's largest value.
+ * magnitude (0 for a block of zeros): mxfp8_quantize's rule with E2M1's largest value.  A block with a NaN has e = 255
+ * and reads back as NaN; an infinity is the largest code under e = 253 and reads back as infinity.
  * A page holds page_size tokens of every head as [head][group of 16 tokens][record]; a record is 17 * head_dim
  * bytes (key codes, value codes, key exponents, value exponents) in the order that the attention kernel's
  * matrix instructions take; csrc/kv4.cuh has it byte by byte.  Token t of sequence s is in page
@@ -411,8 +412,9 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
  * statistics and sums are fp32.  Queries enter as f16, scaled row by row so that their 8 bits are kept down to 2^-27
  * of the row's largest magnitude, and weights with 11 bits; but in a call with a workspace and 96 or more rows of a
  * key/value head per sequence (rows / batch, rounded up, times g) queries enter exactly and weights with 8 bits, and
- * products are bf16 (values past 2^100 may overflow there).  Which of the two a row gets goes by its call.  Rows of a
- * sequence with a page id outside the pool are unspecified.
+ * products are bf16 (values past 2^100 may overflow there).  Which of the two a row gets goes by its call.  For few rows
+ * blocks with e = 0 (magnitudes up to 6 * 2^-127) may count as zeros.  A NaN in a key makes the rows that see it NaN, in
+ * a value the 32 elements of its block.  Rows of a sequence with a page id outside the pool are unspecified.
  *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned
  *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
  *        empty row

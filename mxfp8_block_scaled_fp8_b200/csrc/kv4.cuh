@@ -6,7 +6,9 @@
 // head dimension (value = code * 2^(e - 127)); e is the smallest power of two
 // with 6 * 2^(e - 127) >= the block's largest magnitude, so no element
 // saturates, 0 for a block of zeros: the library's MX rule (the maximum's
-// scale rounded up to a power of two) with E2M1's largest value 6.
+// scale rounded up to a power of two) with E2M1's largest value 6.  255 marks a
+// block with a NaN, as in MX, with codes of zero (0 * inf is NaN); an infinity is
+// the code 6 under 253, the largest exponent of a number.
 //
 // Record.  The unit is one head's 16 consecutive tokens ("group"), 17 * D
 // bytes, in the order in which the attention kernel's matrix instructions
@@ -107,6 +109,8 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&y)[8]) {
 __device__ __forceinline__ float ue8m0_to_f32(uint32_t e) {
   return __uint_as_float(e == 0 ? 0x00400000u : e << 23);
 }
+// The top bits of those bytes of w that are 255.
+__device__ __forceinline__ uint32_t bytes_255(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u; }
 
 // Exponent byte of a block whose largest bf16 magnitude has the bits m (sign
 // cleared): amax = (1 + f / 128) 2^(E - 127) <= 6 * 2^(e - 127) = 1.5 *
@@ -253,7 +257,8 @@ __device__ __forceinline__ void quantize_group(const uint4 (&v)[2][D / 32], uint
                             __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
       m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const uint32_t ex = mxfp4_exponent(max(m & 0xFFFFu, m >> 16));
+      m = max(m & 0xFFFFu, m >> 16);
+      const uint32_t ex = mxfp4_exponent(m);
       e[h][b] = ex;
       const float s = __uint_as_float((254u - min(ex, 253u)) << 23);  // 2^(127 - e), a normal power of two
       float f[8];
@@ -261,6 +266,7 @@ __device__ __forceinline__ void quantize_group(const uint4 (&v)[2][D / 32], uint
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] *= s;
       code[h][b] = f32x8_to_e2m1(f);
+      if (m > 0x7F80u) e[h][b] = 255u, code[h][b] = 0u;  // a NaN
     }
 }
 

@@ -271,7 +271,7 @@ struct AttnWarp {
   }
   __device__ __forceinline__ void set_ref(int b, int e) {
     unit[b] = __uint_as_float(static_cast<uint32_t>(254 + kBias - e) << 23);
-    ref_half = (b == 0 ? 0x80808080u : ref_half) | static_cast<uint32_t>(min(e >> 1, 127)) << (8 * b);
+    ref_half = (b == 0 ? 0x80808080u : ref_half) | static_cast<uint32_t>(min(e >> 1, 126)) << (8 * b);  // 255: never below
   }
 
   // The tile's rows, row0 on: this lane's part of column g of each tile.
@@ -317,8 +317,7 @@ struct AttnWarp {
         for (int i = 0; i < 8; ++i) f[i] = f[i] * f0 * f1;  // one after the other: f0 f1 may be 2^140
         to.frag[t][b][lane] = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
       }
-      // key exponents count one up: one factor 2 to take back
-      if (c == 0 && 8 * t + g < R) to.factor[8 * t + g] = scale2(fabsf(p.scale_log2), -ex - 1);
+      if (c == 0 && 8 * t + g < R) to.factor[8 * t + g] = scale2(fabsf(p.scale_log2), -ex);
     }
   }
 
@@ -365,12 +364,13 @@ struct AttnWarp {
       vw[j] = v.x, vw[j + 1] = v.y, vw[j + 2] = v.z, vw[j + 3] = v.w;
     }
   }
-  // 2^(byte b of w - 127) as fp32 (0 for a byte of 0).
+  // 2^(byte b of w - 127) as fp32; 0 for a byte of 0: such blocks, of magnitudes up to 6 * 2^-127, count as zeros in scores
+  // and in the fast path's sums.
   static __device__ __forceinline__ float exp_byte(uint32_t w, int b) {
     return __uint_as_float((b == 3 ? w >> 1 : w << (23 - 8 * b)) & 0x7F800000u);
   }
 
-  // S^T of one score tile (FOLD groups at rec) into x, not yet scaled.
+  // S^T of one score tile (FOLD groups at rec) into x, not yet scaled; NaN for a key with a NaN (0 * 2^128).
   __device__ __forceinline__ void scores(const Query& q, const uint8_t* rec, float (&x)[NT][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
     uint32_t kw[FOLD][2][NB];
@@ -378,9 +378,9 @@ struct AttnWarp {
     for (int f = 0; f < FOLD; ++f)
 #pragma unroll
       for (int h = 0; h < 2; ++h) load_keys(rec + f * 17 * D, h, kw[f][h]);
-    // exponents of the lane's tokens, one up (the factor 2 is in sc), so that 0 is no zero
+    // exponents of the lane's tokens
     const uint8_t* er = rec + fold() * 17 * D + 16 * D + g * NB;
-    const uint32_t k0 = load_exponents<NB>(er) + 0x01010101u, k1 = load_exponents<NB>(er + 8 * NB) + 0x01010101u;
+    const uint32_t k0 = load_exponents<NB>(er), k1 = load_exponents<NB>(er + 8 * NB);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float d[NT][4];
@@ -485,6 +485,35 @@ struct AttnWarp {
     }
   }
 
+  // Value blocks with a NaN: into the sums of the rows that see their tokens, and their exponents out of the way.  end:
+  // positions of the lane's tokens.
+  __device__ __forceinline__ void put_nan(uint32_t (&ve)[U][2], const int (&end)[U][2]) {
+    const float nan = __int_as_float(0x7FC00000);
+    uint32_t hit[NT][2] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t values = bytes_255(ve[u][h]);
+        ve[u][h] &= ~((values >> 7) * 0xFFu);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (end[u][h] < vis[t][k]) hit[t][k] |= values;
+      }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) hit[t][k] |= __shfl_xor_sync(0xFFFFFFFFu, hit[t][k], off);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          if ((hit[t][k] >> (8 * (j / 2) + 7)) & 1u) o[t][j][k] = o[t][j][k + 2] = nan;
+      }
+  }
+
   // The same with masks, a new maximum or new references.
   template <typename F>
   __device__ __forceinline__ void step_slow(float (&x)[U][NT][4], const uint8_t* rec, uint32_t (&ve)[U][2],
@@ -494,6 +523,7 @@ struct AttnWarp {
     int top[U][2];    // exponents of the largest weights of the lane's tokens (p < 2^top)
     int drop = 1000;  // how far the references may fall: the maxima's least rise
     int end[U][2];    // position of the lane's tokens, INT_MAX where there is no record
+    uint32_t nan = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -503,7 +533,9 @@ struct AttnWarp {
         end[u][h] = at;
         top[u][h] = -1000;
         if (at >= len) ve[u][h] = 0;  // exponents of tokens behind the sequence may be anything
+        nan |= bytes_255(ve[u][h]);
       }
+    if (__builtin_expect(__any_sync(0xFFFFFFFFu, nan != 0), 0)) put_nan(ve, end);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -717,13 +749,13 @@ __device__ __forceinline__ void attn_store(const KvAttnArgs& p, int lo, int rho,
                                            const float (&acc)[4], float mx, float sum) {
   const int64_t i = rho / p.group;
   const int64_t h = head * static_cast<int64_t>(p.group) + (rho - i * p.group);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
   const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
   *reinterpret_cast<uint2*>(p.out + (lo + i) * p.o_st + h * p.o_sh + 4 * d4) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   if (p.lse != nullptr && d4 == 0)
-    p.lse[(lo + i) * p.lse_st + h] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    p.lse[(lo + i) * p.lse_st + h] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // The rows `done` of a tile that one warp has done alone.
@@ -734,7 +766,7 @@ __device__ __forceinline__ void attn_store_warp(const KvAttnArgs& p, const AttnP
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) inv[t][k] = w.l[t][k] > 0.f ? 1.f / w.l[t][k] : 0.f;
+    for (int k = 0; k < 2; ++k) inv[t][k] = w.l[t][k] != 0.f ? 1.f / w.l[t][k] : 0.f;
   w.elements([&](int t, int k, int row, int d, float v) {
     const int rho = pc.row0 + row;
     if (((done >> row) & 1u) == 0) return;
@@ -742,7 +774,7 @@ __device__ __forceinline__ void attn_store_warp(const KvAttnArgs& p, const AttnP
     const int h = pc.head * p.group + (rho - i * p.group);
     p.out[static_cast<int64_t>(pc.q.lo + i) * p.o_st + h * p.o_sh + d] = __float2bfloat16_rn(v * inv[t][k]);
     if (p.lse != nullptr && d == 0)
-      p.lse[static_cast<int64_t>(pc.q.lo + i) * p.lse_st + h] = w.l[t][k] > 0.f ? (w.m[t][k] + log2f(w.l[t][k])) * kLn2 : -INFINITY;
+      p.lse[static_cast<int64_t>(pc.q.lo + i) * p.lse_st + h] = w.l[t][k] != 0.f ? (w.m[t][k] + log2f(w.l[t][k])) * kLn2 : -INFINITY;
   });
 }
 

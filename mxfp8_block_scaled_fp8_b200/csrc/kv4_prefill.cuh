@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
           const int tok = rho / p.group, h = head * p.group + (rho - tok * p.group);
           if (!whole) part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * (kPreRows * (D + 2));
           else out = p.out + static_cast<int64_t>(lo + tok) * p.o_st + h * p.o_sh;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
             uint32_t o[32];
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
             part[kPreRows * D + 128 * t + r] = m;
             part[kPreRows * D + kPreRows + 128 * t + r] = l;
           } else if (row && p.lse != nullptr) {
-            p.lse[static_cast<int64_t>(lo + tok) * p.lse_st + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            p.lse[static_cast<int64_t>(lo + tok) * p.lse_st + h] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
           }
           tc_fence_before();
         }

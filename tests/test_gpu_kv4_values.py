@@ -161,3 +161,54 @@ def test_outlier_values_that_other_rows_see(dim, size, rows, group):
             for h in range(heads * group):
                 kk, vv = (x[:n - rows + i + 1, h // group] for x in written[2])
                 _check_row(out[i, h], lse[i, h], q[i, h], kk, vv, 1.0, weights)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,group", [(1, 2), (6, 3), (70, 3)])
+def test_poisoned_prefix(dim, rows, group):
+    """A NaN that every row sees: in a key it makes the rows NaN, in a value its block of them."""
+    n, heads = 150, 2
+    q = torch.randn(rows, heads * group, dim, generator=torch.Generator().manual_seed(2)).bfloat16()
+    for where in "kv":
+        k, v = (x.float() for x in _kv(n, heads, dim, 6))
+        (k if where == "k" else v)[9, :, 37] = math.nan
+        written = _written(k.bfloat16(), v.bfloat16())
+        for ws, weights in _kinds(rows, group, dim):
+            out, lse = _run(q, written, heads, dim ** -0.5, ws)
+            if where == "k":
+                assert torch.isnan(out).all() and torch.isnan(lse).all()
+                continue
+            assert torch.isnan(out[..., 32:64]).all() and torch.isfinite(lse).all()
+            rest = [d for d in range(dim) if not 32 <= d < 64]
+            for i in range(rows):
+                for h in range(heads * group):
+                    kk, vv = (x[:n - rows + i + 1, h // group] for x in written[2])
+                    s = torch.softmax(kk @ q[i, h].double() * dim ** -0.5, 0)
+                    want, mag = s @ vv[:, rest], s @ vv[:, rest].abs()
+                    assert ((out[i, h, rest] - want).abs() <= 2.0 ** -8 * want.abs() + (weights + 2.0 ** -20) * mag).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_nan_and_infinity_in_the_cache(dim):
+    """A block that holds a NaN has exponent 255 and reads back as NaN; an infinity reads back as infinity; other
+    blocks and tokens are as without."""
+    k, v = _kv(20, 2, dim, 3)
+    clean = _written(k, v)
+    k, v = k.clone(), v.clone()
+    k[3, 1, 40], v[17, 0, 1] = math.nan, math.nan
+    k[4, 0, 2], v[0, 1, 33] = math.inf, -math.inf
+    k[5, 0, 0] = torch.tensor([0x7F81], dtype=torch.int16).view(torch.bfloat16)[0]      # a NaN of the smallest mantissa
+    written = _written(k, v)
+    at = ref.places(dim)
+    got, was = (c[0].cpu().view(2, 2, 17 * dim)[c[1][0].cpu().long()] for c in (written, clean))   # group, head, byte
+    assert got[0, 1, at["ke"][3, 1]] == 255 and got[1, 0, at["ve"][1, 0]] == 255 and got[0, 0, at["ke"][5, 0]] == 255
+    assert got[0, 0, at["ke"][4, 0]] == 253 and got[0, 1, at["ve"][0, 1]] == 253
+    gk, gv = fp8mm.mxfp4_kv_gather(*written[:2], _i32([0, 20]), 16, dim, 20)
+    wk, wv = fp8mm.mxfp4_kv_gather(*clean[:2], _i32([0, 20]), 16, dim, 20)
+    assert torch.isnan(gk[3, 1, 32:64]).all() and torch.isnan(gv[17, 0, :32]).all() and torch.isnan(gk[5, 0, :32]).all()
+    assert gk[4, 0, 2] == math.inf and gv[0, 1, 33] == -math.inf
+    for x, y, blocks in ((gk, wk, ((3, 1, 1), (5, 0, 0), (4, 0, 0))), (gv, wv, ((17, 0, 0), (0, 1, 1)))):
+        for t, h, b in blocks:
+            y[t, h, 32 * b:32 * b + 32] = x[t, h, 32 * b:32 * b + 32]
+        same = (x == y) | (torch.isnan(x) & torch.isnan(y))
+        assert same.all()
