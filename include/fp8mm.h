@@ -414,7 +414,8 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
  * key/value head per sequence (rows / batch, rounded up, times g) queries enter exactly and weights with 8 bits, and
  * products are bf16 (values past 2^100 may overflow there).  Which of the two a row gets goes by its call.  For few rows
  * blocks with e = 0 (magnitudes up to 6 * 2^-127) may count as zeros.  A NaN in a key makes the rows that see it NaN, in
- * a value the 32 elements of its block.  Rows of a sequence with a page id outside the pool are unspecified.
+ * a value the 32 elements of its block, or makes them 2^100 and more where the rows are many and not all rows of the
+ * chunk see it; other rows are not touched.  Rows of a sequence with a page id outside the pool are unspecified.
  *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned
  *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
  *        empty row

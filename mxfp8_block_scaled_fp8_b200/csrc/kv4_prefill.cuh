@@ -298,6 +298,8 @@ struct PreKeys {
   static constexpr int NB = D / 32;
   uint32_t w[2][NB], e[2];
 
+  // (a score is written over where a row does not see its token)
+  static __device__ __forceinline__ void make_finite(uint8_t*, int) {}
   __device__ __forceinline__ void load(const uint8_t* rec, int, int) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
 #pragma unroll
@@ -379,6 +381,20 @@ struct PreValues {
               *reinterpret_cast<const uint32_t*>(&r);
         }
       }
+    }
+  }
+  // What this lane stored: infinities and NaN become the type's largest, so that the weights of 0 of rows that do not see
+  // their tokens leave them out.
+  static __device__ __forceinline__ void make_finite(uint8_t* tile, int at) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll 1
+    for (int i = 0; i < 4 * NJ; ++i) {
+      const int d = 16 * (i >> 2) + g + 8 * (i & 1), chunk = 2 * at + ((i >> 1) & 1);
+      uint32_t* at32 = reinterpret_cast<uint32_t*>(tile + d * 128 + ((chunk ^ g) << 4) + 4 * c);
+      uint32_t v = *at32;
+      if ((v & 0x7F80u) == 0x7F80u) v = (v & 0xFFFF8000u) | 0x7F7Fu;
+      if ((v & 0x7F800000u) == 0x7F800000u) v = (v & 0x8000FFFFu) | 0x7F7F0000u;
+      *at32 = v;
     }
   }
 };
@@ -529,6 +545,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
       if (warp >= 8 && warp < 14) {
         // ---- records to bf16 tiles
         const int groups = (len + kGroup - 1) / kGroup, seq = pc.s, units = (k1 - k0) * kPreGroups;
+        const int first_sees = len - n + row0 / p.group + 1;
         // this warp's groups of the piece: first, first + warps, ..; one is
         // written while the next is on its way
         auto bring = [&](auto rec, int which, int first, int warps) {
@@ -550,7 +567,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
             auto cur = rec;
             if (unit + warps < units) load(n + 1);
             if (!warp_wait(&sh.empty[which][st], ((it / kPreStages) & 1) ^ 1, timeout, abort, kSiteKvRecord)) break;
-            cur.store(smem + Cfg::kQBytes + (which * kPreStages + st) * Cfg::kTileBytes, unit % kPreGroups);
+            uint8_t* tile = smem + Cfg::kQBytes + (which * kPreStages + st) * Cfg::kTileBytes;
+            cur.store(tile, unit % kPreGroups);
+            if ((k0 * kPreGroups + unit + 1) * kGroup > first_sees) cur.make_finite(tile, unit % kPreGroups);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.full[which][st]);

@@ -163,6 +163,36 @@ def test_outlier_values_that_other_rows_see(dim, size, rows, group):
                 _check_row(out[i, h], lse[i, h], q[i, h], kk, vv, 1.0, weights)
 
 
+POISON = {"inf": math.inf, "-inf": -math.inf, "nan": math.nan, "largest": 3.3895313892515355e38}
+
+
+@pytest.mark.parametrize("kind", list(POISON))
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,group", [(1, 2), (4, 2), (6, 3), (70, 3)])
+def test_poisoned_tokens_stay_with_the_rows_that_see_them(kind, where, dim, rows, group):
+    """One element of the last two tokens (a padded step's) is infinite, NaN or the type's largest: rows before them are as without."""
+    n, heads = 150, 2
+    k, v = (x.float() for x in _kv(n, heads, dim, 6))
+    (k if where == "k" else v)[n - 2:, :, 5] = POISON[kind]
+    written = _written(k.bfloat16(), v.bfloat16())
+    q = torch.randn(rows, heads * group, dim, generator=torch.Generator().manual_seed(2)).bfloat16()
+    for ws, weights in _kinds(rows, group, dim):
+        out, lse = _run(q, written, heads, dim ** -0.5, ws)
+        for i in range(rows):
+            seen = n - rows + i + 1
+            for h in range(heads * group):
+                kk, vv = (x[:seen, h // group] for x in written[2])
+                if seen <= n - 2:
+                    _check_row(out[i, h], lse[i, h], q[i, h], kk, vv, dim ** -0.5, weights)
+                elif kind == "nan" and where == "k":
+                    assert torch.isnan(out[i, h]).all() and torch.isnan(lse[i, h])
+                elif kind != "largest" and where == "v":                   # the poisoned block, and no other
+                    hit = out[i, h, :32]
+                    assert (~torch.isfinite(hit) | (hit.abs() > 2.0 ** 100)).any()
+                    _check_row(out[i, h, 32:], lse[i, h], q[i, h], kk, vv[:, 32:], dim ** -0.5, weights)
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("rows,group", [(1, 2), (6, 3), (70, 3)])
 def test_poisoned_prefix(dim, rows, group):
