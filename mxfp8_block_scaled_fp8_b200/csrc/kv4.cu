@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <limits>
 #include <memory>
 #include <new>
 
@@ -234,7 +235,8 @@ fp8mm_status mxfp4_kv_attention(const void* q_bf16, int64_t q_stride_t, int64_t 
   p.rows = rows;
   p.batch = static_cast<int32_t>(cache->batch);
   p.group = static_cast<int32_t>(q_heads / cache->kv_heads);
-  if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = 1e-30f;  // a masked score stays -inf after scaling
+  // a masked score stays -inf after scaling, any other one becomes next to nothing
+  if (p.scale_log2 == 0.f) p.scale_log2 = std::numeric_limits<float>::denorm_min();
   p.timeout_ns = wait_timeout_ns();
   if (workspace != nullptr) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);

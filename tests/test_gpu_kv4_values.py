@@ -11,6 +11,7 @@ good): n tokens are off by n * 6 * 2^-25 of the block's largest |sum|, and that 
 is at most the sum of weight * (largest |v| of the block): n * 2^-22 of that.  Nothing counts that the row does not see."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -242,3 +243,23 @@ def test_nan_and_infinity_in_the_cache(dim):
             y[t, h, 32 * b:32 * b + 32] = x[t, h, 32 * b:32 * b + 32]
         same = (x == y) | (torch.isnan(x) & torch.isnan(y))
         assert same.all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [2, 40])
+@pytest.mark.parametrize("scale", [1e-35, -1e-35, 1e-40])
+def test_scales_of_any_size(dim, rows, scale):
+    """Scales below 1e-30 with queries that make scores of them."""
+    n, heads, group = 150, 2, 3
+    written = _written(*_kv(n, heads, dim, 6))
+    # scores of some tens; for 1e-40 below 1e-2, since products have to be within fp32
+    size = min(0.1 / abs(scale), 2.0 ** 117)
+    q = torch.randn(rows, heads * group, dim, generator=torch.Generator().manual_seed(2)) * size
+    q = q.bfloat16()
+    for ws, weights in _kinds(rows, group, dim):
+        out, lse = _run(q, written, heads, scale, ws)
+        for i in range(rows):
+            for h in range(heads * group):
+                kk, vv = (x[:n - rows + i + 1, h // group] for x in written[2])
+                # the call's scale is a float
+                _check_row(out[i, h], lse[i, h], q[i, h], kk, vv, float(np.float32(scale)), weights)
