@@ -386,7 +386,8 @@ size_t mxfp4_kv_page_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim
 
 /* Ragged batches (the next three calls): rows [cu_seqlens[s], cu_seqlens[s + 1]) belong to sequence s
  * (int32 device, batch + 1 entries, cu_seqlens[0] >= 0, rising); cu_seqlens NULL means one row per sequence
- * (rows == batch).  Rows behind cu_seqlens[batch] are padding: not read, and outputs left as they were.
+ * (rows == batch).  Rows before cu_seqlens[0] and from cu_seqlens[batch] on are padding: not read, and outputs left as
+ * they were.
  * Bounds that do not fit are recorded in the device error word and their sequence skipped. */
 
 /* Quantizes new keys and values into the cache: sequence s's rows become its last tokens, positions

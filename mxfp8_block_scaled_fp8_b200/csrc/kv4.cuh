@@ -189,6 +189,7 @@ __device__ __forceinline__ bool kv_span(const int32_t* cu, int batch, int rows, 
     seq = a;
     lo = cu[seq];
     const int64_t next = cu[seq + 1];
+    if (seq == 0 && r < lo) return false;  // rows before the first sequence are padding too
     if (lo < 0 || r < lo || r >= next || next > rows) {
       record_index_error(kSiteSequence);
       return false;

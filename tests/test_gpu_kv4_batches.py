@@ -1,0 +1,72 @@
+"""Batches of the cache operators: bounds that do not begin at row 0, lengths
+that do not fit, many sequences, tables wider than 32 bits of work, single rows
+of any stride, results over the queries, workspaces that were not zeroed.
+Tolerances are those of tests/test_gpu_kv4.py."""
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_block_scaled_fp8_b200 as fp8mm
+from tests import gpu_util as gu
+from tests import kv4_ref as ref
+from tests.test_gpu_kv4 import BF16_WEIGHTS, _check_attention, _filled, _i32, _kv
+
+pytestmark = pytest.mark.gpu
+INDEX, WORKSPACE = 2, 3                                        # kinds of the device error word
+POSITION, SEQUENCE = 16, 17                                    # and places
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    gu.require_gpu()
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert fp8mm.last_device_error() == 0
+
+
+def _workspace(dim):
+    return torch.zeros(fp8mm.mxfp4_kv_attention_workspace_bytes(dim), dtype=torch.uint8, device="cuda")
+
+
+def _queries(n, heads, dim, seed=1):
+    return torch.randn(n, heads, dim, generator=torch.Generator().manual_seed(seed)).bfloat16()
+
+
+@pytest.mark.parametrize("first", [1, 5, 40])
+@pytest.mark.parametrize("new", [[1, 3, 0, 1], [70, 64, 1, 90]])
+def test_bounds_that_begin_behind_row_0(first, new):
+    """Rows before cu_seqlens[0] belong to no sequence: not read, results as they were, no error."""
+    dim, hk, hq, ps = 64, 2, 4, 16
+    rng = np.random.default_rng(4)
+    old = [20, 7, 33, 0]
+    lengths = [a + b for a, b in zip(old, new)]
+    cache, table, own = _filled(rng, lengths, ps, hk, dim, 3)
+    cu = (first + np.concatenate([[0], np.cumsum(new)])).tolist()
+    rows = cu[-1] + 2
+    k, v = _kv(rows, hk, dim, 9)
+    k[:first], v[:first] = float("nan"), float("nan")
+    (kc, ke), (vc, ve) = ref.quantize(torch.nan_to_num(k)), ref.quantize(torch.nan_to_num(v))
+    dev = cache.data.cuda()
+    for s, n in enumerate(new):
+        for t in range(n):
+            r, pos = cu[s] + t, old[s] + t
+            cache.write(own[s][pos // ps], pos % ps, kc[r], ke[r], vc[r], ve[r])
+    fp8mm.mxfp4_kv_append(k.cuda(), v.cuda(), dev, _i32(table), _i32(lengths), ps, cu_seqlens=_i32(cu))
+    assert fp8mm.last_device_error() == 0
+    assert torch.equal(dev.cpu(), cache.data)
+    gk, gv = (torch.full((rows, hk, dim), 7, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    fp8mm.mxfp4_kv_gather(dev, _i32(table), _i32(cu), ps, dim, rows, starts=_i32(old), k=gk, v=gv)
+    assert fp8mm.last_device_error() == 0
+    for got, codes, e in ((gk, kc, ke), (gv, vc, ve)):
+        want = ref.value(codes, e).bfloat16()
+        assert torch.equal(got[first:cu[-1]].cpu(), want[first:cu[-1]]) and (got[:first] == 7).all() and (got[cu[-1]:] == 7).all()
+    q = _queries(rows, hq, dim)
+    for ws in (_workspace(dim), None):
+        out = torch.full((rows, hq, dim), 5, dtype=torch.bfloat16, device="cuda")
+        fp8mm.mxfp4_kv_attention(q.cuda(), dev, _i32(table), _i32(lengths), ps, cu_seqlens=_i32(cu), out=out, workspace=ws)
+        many = ws is not None and -(-rows // 4) * 2 >= 96
+        _check_attention(out, None, q, cache, own, lengths, cu, dim ** -0.5, BF16_WEIGHTS if many else 2.0 ** -10)
+        assert (out[:first] == 5).all() and (out[cu[-1]:] == 5).all()
