@@ -445,10 +445,12 @@ fp8mm_status kv_copy_pages(void* pages, int64_t num_pages, int64_t page_bytes, i
 const char* fp8mm_status_str(fp8mm_status status);
 /* CUDA error code of the last failed CUDA call made by the library (0 if none). */
 int fp8mm_last_cuda_error(void);
-/* Synchronizes the current device, returns the device error word (0 = none;
+/* Synchronizes the current device, returns a device error word (0 = none;
  * bits 0-7 kind (1 = bounded wait expired, 2 = an index in device memory out of
  * range: site 16 a position, 17 a sequence's bounds or length, 18 a page id),
- * 8-15 site, 16-31 CTA) and clears it. */
+ * 8-15 site, 16-31 CTA) and clears it.  The matrix products and quantizers have
+ * one word, the cache's operators another, each of the first error since it was
+ * read: a call returns the first of them that is set. */
 unsigned int fp8mm_last_device_error(void);
 /* Self-test of the bounded wait: launches one CTA that waits on an mbarrier
  * nothing will ever arrive at, with a limit of timeout_us microseconds, and

@@ -1045,8 +1045,7 @@ unsigned int fp8mm_last_device_error(void) {
   if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
   const unsigned int zero = 0;
   cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
-  const unsigned int kv = kv_take_device_error();
-  return v != 0 ? v : kv;
+  return v != 0 ? v : kv_take_device_error();  // the other word stays for the next call
 }
 
 fp8mm_status fp8mm_selftest_wait_timeout(uint32_t timeout_us, void* stream) {

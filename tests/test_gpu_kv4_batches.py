@@ -70,3 +70,17 @@ def test_bounds_that_begin_behind_row_0(first, new):
         many = ws is not None and -(-rows // 4) * 2 >= 96
         _check_attention(out, None, q, cache, own, lengths, cu, dim ** -0.5, BF16_WEIGHTS if many else 2.0 ** -10)
         assert (out[:first] == 5).all() and (out[cu[-1]:] == 5).all()
+
+
+def test_error_words_of_both_kinds_are_kept():
+    """An expired wait of a GEMM and a bad position stand side by side: each is reported, one after the other."""
+    assert fp8mm.last_device_error() == 0
+    a = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    cs = torch.zeros(1, 64, device="cuda")
+    for _ in range(2):
+        fp8mm.qk_norm_rope(a, a, cs, _i32([7]))
+        L = fp8mm.fp8mm.lib()
+        assert L.fp8mm_selftest_wait_timeout(2000, None) == fp8mm.fp8mm.FP8MM_ERR_DEVICE
+        word = fp8mm.last_device_error()
+        assert (word & 0xFF, word >> 8 & 0xFF) == (INDEX, POSITION)
+        assert fp8mm.last_device_error() == 0
