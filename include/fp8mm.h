@@ -388,7 +388,8 @@ size_t mxfp4_kv_page_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim
  * (int32 device, batch + 1 entries, cu_seqlens[0] >= 0, rising); cu_seqlens NULL means one row per sequence
  * (rows == batch).  Rows before cu_seqlens[0] and from cu_seqlens[batch] on are padding: not read, and outputs left as
  * they were.
- * Bounds that do not fit are recorded in the device error word and their sequence skipped. */
+ * Bounds and lengths that do not fit (a length that is negative, past its row of the page table, or within 64 of 2^31)
+ * are recorded in the device error word and their sequence skipped. */
 
 /* Quantizes new keys and values into the cache: sequence s's rows become its last tokens, positions
  * seq_lens[s] - (rows of s) .. seq_lens[s] - 1, seq_lens (int32 device) counting them.  seq_lens[s] == 0

@@ -36,6 +36,8 @@
 namespace fp8mm {
 
 constexpr int kGroup = 16;  // tokens of a record
+// Tokens of a sequence at most: below it no position of a last step passes an int.
+constexpr int kMostTokens = 0x7FFFFFFF - 64;
 
 struct KvCache {
   uint8_t* base;
@@ -203,7 +205,7 @@ __device__ __forceinline__ bool kv_span(const int32_t* cu, int batch, int rows, 
     if (lens[seq] == 0) return false;  // a padding sequence: nothing of it is kept
     start = static_cast<int64_t>(lens[seq]) - n;
   }
-  if (start < 0 || start + n > INT32_MAX - kGroup) {
+  if (start < 0 || start + n > kMostTokens) {
     record_index_error(kSiteSequence);
     return false;
   }

@@ -165,10 +165,10 @@ __device__ __forceinline__ AttnSeq attn_seq(const KvAttnArgs& p, int s) {
     q.n = 0;
   }
   q.len = p.lens[s];
-  const int most = p.kv.max_pages * p.kv.page_groups * kGroup;  // fits: checked on the host
+  const int most = min(p.kv.max_pages * p.kv.page_groups * kGroup, kMostTokens);  // fits: checked on the host
   if (q.len < 0 || q.len > most) {
     record_index_error(kSiteSequence);
-    q.len = max(0, min(q.len, most));
+    q.n = q.len = 0;
   }
   // rows of a head below 2^31: checked on the host
   q.tiles = (static_cast<uint32_t>(q.n) * p.group + R - 1) / R * p.kv.kv_heads;

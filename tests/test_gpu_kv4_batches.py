@@ -72,6 +72,28 @@ def test_bounds_that_begin_behind_row_0(first, new):
         assert (out[:first] == 5).all() and (out[cu[-1]:] == 5).all()
 
 
+@pytest.mark.parametrize("new,hq,hk", [([1, 1, 1], 4, 2), ([70, 64, 70], 4, 2)])
+@pytest.mark.parametrize("bad", [113, 1 << 30, (1 << 31) - 1, -1, -(1 << 31)])
+def test_lengths_that_do_not_fit(new, hq, hk, bad):
+    """A sequence whose length is negative, or longer than its row of the page table, is recorded and skipped."""
+    dim, lengths = 64, [100, 112, 80]
+    cache, table, own = _filled(np.random.default_rng(4), lengths, 16, hk, dim, 3)
+    dev, cu = cache.data.cuda(), np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = _queries(cu[-1], hq, dim)
+    for ws in (_workspace(dim), None):
+        out = torch.full((cu[-1], hq, dim), 5, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((cu[-1], hq), 5.0, device="cuda")
+        fp8mm.mxfp4_kv_attention(q.cuda(), dev, _i32(table), _i32([100, bad, 80]), 16, cu_seqlens=_i32(cu), out=out, lse=lse,
+                                 workspace=ws)
+        word = fp8mm.last_device_error()
+        assert (word & 0xFF, word >> 8 & 0xFF) == (INDEX, SEQUENCE)
+        assert (out[cu[1]:cu[2]] == 5).all() and (lse[cu[1]:cu[2]] == 5).all()
+        lim = BF16_WEIGHTS if ws is not None and new[0] > 1 else 2.0 ** -10
+        for s in (0, 2):
+            rows = slice(cu[s], cu[s + 1])
+            _check_attention(out[rows], lse[rows], q[rows], cache, [own[s]], [lengths[s]], [0, new[s]], dim ** -0.5, lim)
+
+
 def test_error_words_of_both_kinds_are_kept():
     """An expired wait of a GEMM and a bad position stand side by side: each is reported, one after the other."""
     assert fp8mm.last_device_error() == 0
@@ -84,3 +106,23 @@ def test_error_words_of_both_kinds_are_kept():
         word = fp8mm.last_device_error()
         assert (word & 0xFF, word >> 8 & 0xFF) == (INDEX, POSITION)
         assert fp8mm.last_device_error() == 0
+
+
+def test_lengths_next_to_2_to_the_31():
+    """A table with room for 2^31 - 16 tokens (of one page, repeated): lengths within 64 of 2^31, whose positions would
+    pass an int, are recorded and nothing is done."""
+    dim, ps, hk = 64, 16, 1
+    most = (2 ** 31 - 1) // ps
+    cache = torch.zeros(1, fp8mm.mxfp4_kv_page_bytes(ps, hk, dim), dtype=torch.uint8, device="cuda")
+    table = torch.zeros(1, most, dtype=torch.int32, device="cuda")
+    assert most * ps > 2 ** 31 - 20
+    bad = _i32([2 ** 31 - 20])
+    q, x = _queries(200, 4, dim).cuda(), _queries(200, 1, dim).cuda()
+    for rows, ws in ((1, None), (1, _workspace(dim)), (200, _workspace(dim))):
+        out = torch.full_like(q, 5)
+        fp8mm.mxfp4_kv_attention(q, cache, table, bad, ps, cu_seqlens=_i32([0, rows]), out=out, workspace=ws)
+        word = fp8mm.last_device_error()
+        assert (word & 0xFF, word >> 8 & 0xFF) == (INDEX, SEQUENCE) and (out == 5).all()
+    fp8mm.mxfp4_kv_append(x, x, cache, table, bad, ps, cu_seqlens=_i32([0, 200]))
+    word = fp8mm.last_device_error()
+    assert (word & 0xFF, word >> 8 & 0xFF) == (INDEX, SEQUENCE) and not cache.any()
