@@ -422,8 +422,9 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
  *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
  *        empty row
  *   workspace  mxfp4_kv_attention_workspace_bytes(head_dim) bytes, 256-byte aligned, zeroed once before first
- *        use; every call leaves its counters zero.  It lets long sequences be cut over the SMs.  Calls sharing one must
- *        not overlap on the GPU.  NULL: a sequence and head is never cut.
+ *        use (else recorded in the device error word, the results unspecified); every call leaves its counters
+ *        zero.  It lets long sequences be cut over the SMs.  Calls sharing one must not overlap on the GPU.  NULL: a
+ *        sequence and head is never cut.
  * q must be finite.  Slots behind a sequence may hold any bytes. */
 fp8mm_status mxfp4_kv_attention(const void* q_bf16, int64_t q_stride_t, int64_t q_stride_h, int64_t rows,
                                 int64_t q_heads, const int32_t* cu_seqlens, const int32_t* seq_lens,
@@ -448,10 +449,11 @@ const char* fp8mm_status_str(fp8mm_status status);
 int fp8mm_last_cuda_error(void);
 /* Synchronizes the current device, returns a device error word (0 = none;
  * bits 0-7 kind (1 = bounded wait expired, 2 = an index in device memory out of
- * range: site 16 a position, 17 a sequence's bounds or length, 18 a page id),
- * 8-15 site, 16-31 CTA) and clears it.  The matrix products and quantizers have
- * one word, the cache's operators another, each of the first error since it was
- * read: a call returns the first of them that is set. */
+ * range: site 16 a position, 17 a sequence's bounds or length, 18 a page id,
+ * 3 = a workspace of mxfp4_kv_attention that was not zeroed), 8-15 site, 16-31 CTA)
+ * and clears it.  The matrix products and quantizers have one word, the cache's
+ * operators another, each of the first error since it was read: a call returns the
+ * first of them that is set. */
 unsigned int fp8mm_last_device_error(void);
 /* Self-test of the bounded wait: launches one CTA that waits on an mbarrier
  * nothing will ever arrive at, with a limit of timeout_us microseconds, and

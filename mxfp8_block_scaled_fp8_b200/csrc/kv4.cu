@@ -91,10 +91,11 @@ static size_t attn_workspace(int sms, int64_t d) {
 }
 
 template <int D, int NT, int FOLD>
-static fp8mm_status launch_attn(const KvAttnArgs& p, cudaStream_t s, const DeviceInfo& dev) {
+static fp8mm_status launch_attn(KvAttnArgs& p, cudaStream_t s, const DeviceInfo& dev) {
   using Cfg = AttnCfg<D, NT, FOLD>;
   auto kern = kv4_attn_kernel<D, NT, FOLD>;
   const int grid = (NT == 1 ? kAttnCtas : 1) * dev.sms;
+  p.jobs = grid * kAttnWarps;
   const int smem = kAttnWarps * static_cast<int>(sizeof(AttnShared<D, NT, FOLD>));
   fp8mm_status st = ensure_smem(reinterpret_cast<const void*>(kern), smem, dev.device);
   if (st != FP8MM_OK) return st;
@@ -104,8 +105,9 @@ static fp8mm_status launch_attn(const KvAttnArgs& p, cudaStream_t s, const Devic
 }
 
 template <int D>
-static fp8mm_status launch_prefill(const KvAttnArgs& p, cudaStream_t s, const DeviceInfo& dev) {
+static fp8mm_status launch_prefill(KvAttnArgs& p, cudaStream_t s, const DeviceInfo& dev) {
   auto kern = kv4_prefill_kernel<D>;
+  p.jobs = dev.sms;
   fp8mm_status st = ensure_smem(reinterpret_cast<const void*>(kern), PreCfg<D>::kSmemBytes, dev.device);
   if (st != FP8MM_OK) return st;
   st = launch_pdl(kern, dim3(dev.sms), dim3(kPreThreads), PreCfg<D>::kSmemBytes, s, p);

@@ -72,6 +72,7 @@ struct KvAttnArgs {
   struct AttnCut* cuts;  // of the tiles that are cut
   struct AttnCounters* counters;
   int32_t unit_steps;    // steps of a unit: 1, or more where the units would not fit 31 bits
+  int32_t jobs;          // that the grid has: lines of the list
 };
 
 constexpr int kAttnCtas = 2;      // CTAs of an SM (NT = 1)
@@ -83,6 +84,7 @@ constexpr int kAttnStages = 2;    // steps of a warp's ring
 // Zero between calls.
 struct AttnCounters {
   unsigned cut, done;
+  unsigned zero[62];  // always: what a workspace that was not zeroed is known by
 };
 // A tile that is cut over jobs first..last: rows row0.. of a head, of the
 // sequence whose rows begin at lo.
@@ -781,6 +783,22 @@ __device__ __forceinline__ void attn_store_warp(const KvAttnArgs& p, const AttnP
 // Weight of a partial result with maximum m under the joint maximum mx.
 __device__ __forceinline__ float join_weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
 
+// A line of the list of cut tiles.  (The join sees to counters that were not zero: nothing is written past the list.)
+__device__ __forceinline__ void attn_list_cut(const KvAttnArgs& p, const AttnCut& cut) {
+  const unsigned at = atomicAdd(&p.counters->cut, 1u);
+  if (at < static_cast<unsigned>(p.jobs)) p.cuts[at] = cut;
+}
+// The look at a line before it is followed, since in a workspace that was not zeroed it may be anything.
+template <int R>
+__device__ __forceinline__ bool attn_cut_fits(const KvAttnArgs& p, const AttnCut& cut) {
+  if (cut.first >= 0 && cut.first <= cut.last && cut.last < p.jobs && cut.head >= 0 && cut.head < p.kv.kv_heads &&
+      cut.lo >= 0 && cut.row0 >= 0 && cut.rows >= 1 && cut.rows <= R &&
+      cut.lo + static_cast<int64_t>((static_cast<uint32_t>(cut.row0) + cut.rows - 1) / p.group) < p.rows)
+    return true;
+  record_error(kDevErrWorkspace, kSiteKvCuts);
+  return false;
+}
+
 constexpr int kJoinThreads = 256;
 constexpr int kJoinAlone = 32;  // pieces that one warp joins alone
 
@@ -839,18 +857,20 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const KvAtt
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  const unsigned items = p.counters->cut * R;
+  const unsigned lines = p.counters->cut, items = lines <= static_cast<unsigned>(p.jobs) ? lines * R : 0;
+  if (blockIdx.x == 0 && threadIdx.x < 62 && (p.counters->zero[threadIdx.x] != 0 || lines > static_cast<unsigned>(p.jobs)))
+    record_error(kDevErrWorkspace, kSiteKvCounters);
   for (unsigned it = blockIdx.x * W + warp; it < items; it += gridDim.x * W) {
     const AttnCut cut = p.cuts[it / R];
     const int row = it % R;
-    if (row >= cut.rows || cut.last - cut.first >= kJoinAlone) continue;
+    if (row >= cut.rows || cut.last - cut.first >= kJoinAlone || !attn_cut_fits<R>(p, cut)) continue;
     const JoinSum s = attn_join_pieces<D, R>(p, cut, row, 0, 1);
     if (lane < L) attn_store<D>(p, cut.lo, cut.row0 + row, cut.head, lane, s.acc, s.mx, s.sum);
   }
   for (unsigned it = blockIdx.x; it < items; it += gridDim.x) {
     const AttnCut cut = p.cuts[it / R];
     const int row = it % R;
-    if (row >= cut.rows || cut.last - cut.first < kJoinAlone) continue;
+    if (row >= cut.rows || cut.last - cut.first < kJoinAlone || !attn_cut_fits<R>(p, cut)) continue;
     const JoinSum s = attn_join_pieces<D, R>(p, cut, row, warp, W);
     if (lane < L) s_acc[warp][lane] = make_float4(s.acc[0], s.acc[1], s.acc[2], s.acc[3]);
     if (lane == 0) {
@@ -878,7 +898,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attn_join_kernel(const KvAtt
   }
   __syncthreads();
   // the last CTA that has read the list leaves the counters as they were found
-  if (threadIdx.x == 0 && atomicAdd(&p.counters->done, 1u) + 1 == gridDim.x) *p.counters = AttnCounters{0, 0};
+  if (threadIdx.x == 0 && atomicAdd(&p.counters->done, 1u) + 1 == gridDim.x) p.counters->cut = p.counters->done = 0;
 }
 
 // A warp's part of the CTA's shared memory.
@@ -1028,9 +1048,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? kAttnCtas : 1) kv4_att
       continue;
     }
     if (!whole && begins && lane == 0)  // to the list of cut tiles
-      p.cuts[atomicAdd(&p.counters->cut, 1u)] =
-          AttnCut{static_cast<int>(pc.job), static_cast<int>(cut.job_of(pc.i1 - 1)), pc.q.lo, pc.head, pc.row0,
-                  min(pc.q.n * p.group - pc.row0, R)};
+      attn_list_cut(p, AttnCut{static_cast<int>(pc.job), static_cast<int>(cut.job_of(pc.i1 - 1)), pc.q.lo, pc.head, pc.row0,
+                               min(pc.q.n * p.group - pc.row0, R)});
     if (pc.end >= pc.job_end) break;
     __syncwarp();
     if (lane == 0) {

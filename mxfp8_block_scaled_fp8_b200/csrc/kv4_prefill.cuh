@@ -693,8 +693,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
         const int lo = pc.q.lo;
         if (!whole && begins && threadIdx.x == 0) {  // to the list of cut tiles
           const int64_t last = (pc.i1 * jobs - 1) / total;  // the job that holds unit i1 - 1
-          p.cuts[atomicAdd(&p.counters->cut, 1u)] =
-              AttnCut{static_cast<int>(blockIdx.x), static_cast<int>(last), lo, head, row0, min(rows - row0, kPreRows)};
+          attn_list_cut(p, AttnCut{static_cast<int>(blockIdx.x), static_cast<int>(last), lo, head, row0,
+                                   min(rows - row0, kPreRows)});
         }
         // ---- the next piece's queries: every QK of this one is done, since its scores have been read
         if (more && ok) {

@@ -17,7 +17,7 @@ namespace fp8mm {
 // Layout: bits 0..7 error kind, bits 8..15 wait site, bits 16..31 block id.
 static __device__ unsigned int g_device_error = 0;
 
-enum DevErr : unsigned { kDevErrTimeout = 1, kDevErrIndex = 2 };
+enum DevErr : unsigned { kDevErrTimeout = 1, kDevErrIndex = 2, kDevErrWorkspace = 3 };
 
 enum WaitSite : unsigned {
   kSiteProducerEmpty = 1, kSiteMmaFull = 2, kSiteMmaAccEmpty = 3, kSiteEpiAccFull = 4,
@@ -26,6 +26,8 @@ enum WaitSite : unsigned {
   // data errors (kDevErrIndex): which index was out of range
   kSitePosition = 16, kSiteSequence = 17, kSitePage = 18,
   kSiteKvRecord = 19, kSiteKvDrain = 20,
+  // a workspace that was not zeroed (kDevErrWorkspace)
+  kSiteKvCounters = 21, kSiteKvCuts = 22,
 };
 
 __device__ __forceinline__ void record_error(unsigned kind, unsigned site) {

@@ -126,3 +126,25 @@ def test_lengths_next_to_2_to_the_31():
     fp8mm.mxfp4_kv_append(x, x, cache, table, bad, ps, cu_seqlens=_i32([0, 200]))
     word = fp8mm.last_device_error()
     assert (word & 0xFF, word >> 8 & 0xFF) == (INDEX, SEQUENCE) and not cache.any()
+
+
+@pytest.mark.parametrize("new,hq,hk", [([1, 1, 1], 4, 2), ([70, 64, 70], 4, 2)])
+@pytest.mark.parametrize("fill", [255, 1, "random"])
+def test_workspaces_that_were_not_zeroed(new, hq, hk, fill):
+    """Recorded, whatever the bytes say; with the counters zeroed the same workspace serves."""
+    dim, lengths = 64, [3000, 130, 80]
+    cache, table, own = _filled(np.random.default_rng(4), lengths, 16, hk, dim, 3)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q, ws = _queries(cu[-1], hq, dim), _workspace(dim)
+    if fill == "random":
+        ws.random_(0, 256, generator=torch.Generator(device="cuda").manual_seed(3))
+    else:
+        ws.fill_(fill)
+    args = (q.cuda(), cache.data.cuda(), _i32(table), _i32(lengths), 16, _i32(cu))
+    for _ in range(2):
+        fp8mm.mxfp4_kv_attention(*args, workspace=ws)
+        assert fp8mm.last_device_error() & 0xFF == WORKSPACE
+    ws[:256] = 0
+    for _ in range(2):
+        out = fp8mm.mxfp4_kv_attention(*args, workspace=ws)
+        _check_attention(out, None, q, cache, own, lengths, cu, dim ** -0.5, BF16_WEIGHTS if new[0] > 1 else 2.0 ** -10)
