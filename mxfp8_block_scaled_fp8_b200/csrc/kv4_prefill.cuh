@@ -752,7 +752,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv4_prefill_kernel(const KvAtt
       }
       tile0 += k1 - k0;
       filled += k0 < k1;
-      if (!more || *abort != 0) break;
+      // (the whole warp, should its lanes read the flag apart: those that go on wait for all)
+      if (!more || __any_sync(0xFFFFFFFFu, *abort != 0)) break;
       if (warp >= 8) {
         __syncwarp();
         if (lane == 0) pre_next(p, pc);
