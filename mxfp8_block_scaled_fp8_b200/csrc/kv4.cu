@@ -122,7 +122,9 @@ using namespace fp8mm;
 extern "C" {
 
 size_t mxfp4_kv_page_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim) {
-  if (page_size < 16 || page_size % 16 != 0 || kv_heads < 1 || (head_dim != 64 && head_dim != 128)) return 0;
+  if (page_size < 16 || page_size % 16 != 0 || page_size > 4096 || kv_heads < 1 || kv_heads > 65535 ||
+      (head_dim != 64 && head_dim != 128))
+    return 0;
   return static_cast<size_t>(page_bytes(page_size, kv_heads, head_dim));
 }
 

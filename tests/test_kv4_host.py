@@ -278,3 +278,10 @@ def test_reference_quantizer_takes_the_smallest_exponent():
     zero = amax == 0
     assert (e[zero] == 0).all()
     assert (6 * 2.0 ** (e - 127) >= amax).all() and (6 * 2.0 ** (e - 128) < amax)[~zero].all()
+
+
+def test_page_bytes_of_sizes_that_calls_refuse():
+    """0 for the sizes that append, gather and attention refuse, up to the largest that they take."""
+    assert fp8mm.mxfp4_kv_page_bytes(4096, 65535, 128) == 4096 // 16 * 65535 * 17 * 128
+    for bad in ((4112, 1, 64), (8192, 2, 128), (16, 65536, 64), (1 << 40, 1, 64), (16, 1 << 60, 128)):
+        assert fp8mm.mxfp4_kv_page_bytes(*bad) == 0, bad
