@@ -424,10 +424,11 @@ def _tensor(t, dtype, index: int, name: str, shape=None, dims: int = 1):
 
 
 def _heads(t, index: int, name: str, shape=None):
-    """[rows, heads, dim] bf16 -> pointer, row stride, head stride."""
+    """[rows, heads, dim] bf16 -> pointer, row stride, head stride; those of one row, or one head, say nothing."""
     _tensor(t, _BF16, index, name, shape, 3)
+    n, h, d = t.shape
     st = t.stride()
-    return t.data_ptr(), st[0], st[1]
+    return t.data_ptr(), st[0] if n > 1 else h * d, st[1] if h > 1 else d
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: torch.Tensor, positions: torch.Tensor,
@@ -467,7 +468,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: torch.Tensor, positi
         ko = _heads(k_out, dev, "k_out", k.shape)
     cs = cos_sin.shape
     _check("qk_norm_rope", lib().qk_norm_rope(
-        *qa, *ka, t, hq, hk, d, qw, kw, eps, cos_sin.data_ptr(), cs[0], cs[1], cos_sin.stride(0),
+        *qa, *ka, t, hq, hk, d, qw, kw, eps, cos_sin.data_ptr(), cs[0], cs[1], cos_sin.stride(0) if cs[0] > 1 else cs[1],
         1 if interleaved else 0, positions.data_ptr(), *qo, *ko, _raw(dev)))
     return q_out, k_out
 
@@ -487,7 +488,7 @@ def _kv_cache(cache, page_table, page_size: int, head_dim: int, dev: int):
     if one <= 0 or size % one != 0 or size == 0:
         raise ValueError(f"cache: pages of {size} bytes do not hold {page_size} tokens of whole heads of {head_dim}")
     return size // one, batch, KV_CACHE_DESC.pack(
-        cache.data_ptr(), cache.stride(0), pages, page_size, size // one, head_dim, page_table.data_ptr(),
+        cache.data_ptr(), cache.stride(0) if pages > 1 else size, pages, page_size, size // one, head_dim, page_table.data_ptr(),
         page_table.stride(0) if batch > 1 else most, most, batch)
 
 
@@ -608,7 +609,7 @@ def kv_copy_pages(cache: torch.Tensor, src, dst, stream=None) -> torch.Tensor:
         raise ValueError(f"page ids: {e}") from None
     at = ctypes.cast(ids, _P).value
     size = cache.element_size()
-    layers, layer_stride = (shape[0], st[0] * size) if len(shape) == 3 else (1, 0)
+    layers, layer_stride = (shape[0], st[0] * size) if len(shape) == 3 and shape[0] > 1 else (len(shape) == 2 or shape[0], 0)
     _check("kv_copy_pages", lib().kv_copy_pages(cache.data_ptr(), shape[-2], shape[-1] * size, st[-2] * size, layers,
                                                 layer_stride, at, at + 4 * n, n, _raw(dev)))
     return cache

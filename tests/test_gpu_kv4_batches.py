@@ -94,6 +94,31 @@ def test_lengths_that_do_not_fit(new, hq, hk, bad):
             _check_attention(out[rows], lse[rows], q[rows], cache, [own[s]], [lengths[s]], [0, new[s]], dim ** -0.5, lim)
 
 
+def test_single_rows_and_heads_of_any_stride():
+    """The stride of a dimension of one element says nothing: it is not checked."""
+    dim, ps = 64, 16
+    odd = lambda x, stride: x.contiguous().as_strided(x.shape, stride)
+    g = torch.Generator().manual_seed(3)
+    cs = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).cuda()
+    q, k, v = (torch.randn(1, h, dim, generator=g).bfloat16().cuda() for h in (2, 1, 1))
+    cache = torch.zeros(1, fp8mm.mxfp4_kv_page_bytes(ps, 1, dim), dtype=torch.uint8, device="cuda")
+    table, lens = _i32([[0]]), _i32([1])
+    q1, k1, v1 = odd(q, (3, dim, 1)), odd(k, (0, 5, 1)), odd(v, (1, 0, 1))
+    qo, ko = fp8mm.qk_norm_rope(q1, k1, odd(cs, (0, 1)), _i32([0]), q_out=torch.empty_like(q).as_strided(q.shape, (0, dim, 1)))
+    assert torch.equal(qo, q) and torch.equal(ko, k)
+    one = odd(cache, (1, 1))
+    fp8mm.mxfp4_kv_append(k1, v1, one, odd(table, (0, 1)), lens, ps)
+    k2, v2 = (torch.empty_like(k).as_strided(k.shape, (3, 3, 1)) for _ in range(2))
+    fp8mm.mxfp4_kv_gather(one, table, _i32([0, 1]), ps, dim, 1, k=k2, v=v2)
+    assert torch.equal(v2.cpu(), ref.value(*ref.quantize(v.cpu())).bfloat16())
+    out = torch.empty_like(q).as_strided(q.shape, (0, dim, 1))
+    fp8mm.mxfp4_kv_attention(q1, one, table, lens, ps, out=out)
+    assert torch.equal(out, v2.expand(1, 2, dim))
+    layers = torch.arange(64, dtype=torch.uint8, device="cuda").view(1, 4, 16)
+    fp8mm.kv_copy_pages(layers.as_strided(layers.shape, (5, 16, 1)), [0], [3])
+    assert torch.equal(layers[0, 3], layers[0, 0])
+
+
 def test_error_words_of_both_kinds_are_kept():
     """An expired wait of a GEMM and a bad position stand side by side: each is reported, one after the other."""
     assert fp8mm.last_device_error() == 0
