@@ -418,7 +418,7 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
  * blocks with e = 0 (magnitudes up to 6 * 2^-127) may count as zeros.  A NaN in a key makes the rows that see it NaN, in
  * a value the 32 elements of its block, or makes them 2^100 and more where the rows are many and not all rows of the
  * chunk see it; other rows are not touched.  Rows of a sequence with a page id outside the pool are unspecified.
- *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned
+ *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned; out may be q itself
  *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
  *        empty row
  *   workspace  mxfp4_kv_attention_workspace_bytes(head_dim) bytes, 256-byte aligned, zeroed once before first

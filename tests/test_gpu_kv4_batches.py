@@ -9,7 +9,7 @@ import torch
 import mxfp8_block_scaled_fp8_b200 as fp8mm
 from tests import gpu_util as gu
 from tests import kv4_ref as ref
-from tests.test_gpu_kv4 import BF16_WEIGHTS, _check_attention, _filled, _i32, _kv
+from tests.test_gpu_kv4 import BF16_WEIGHTS, _check_attention, _filled, _i32, _kv, _tables
 
 pytestmark = pytest.mark.gpu
 INDEX, WORKSPACE = 2, 3                                        # kinds of the device error word
@@ -94,6 +94,81 @@ def test_lengths_that_do_not_fit(new, hq, hk, bad):
             _check_attention(out[rows], lse[rows], q[rows], cache, [own[s]], [lengths[s]], [0, new[s]], dim ** -0.5, lim)
 
 
+@pytest.mark.parametrize("batch,most", [(40, 5), (700, 4), (1500, 3)])
+def test_append_and_gather_of_many_sequences(batch, most):
+    """More sequences than a warp, and than its square, searches at once, with empty ones at either end and in runs."""
+    rng = np.random.default_rng(batch)
+    new = rng.integers(0, most, batch)
+    new[[0, 1, batch - 1]] = 0
+    new[batch // 3:batch // 3 + 37] = 0
+    new[batch // 2] = 61
+    old = np.where(new > 0, rng.integers(0, 20, batch), 0)
+    lengths = (old + new).tolist()
+    table, own, pages = _tables(rng, lengths, 16)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    cache = ref.Cache(pages, 16, 1, 64, seed=5)
+    dev = cache.data.cuda()
+    k, v = _kv(cu[-1] + 3, 1, 64, 2)
+    (kc, ke), (vc, ve) = ref.quantize(k), ref.quantize(v)
+    for s in range(batch):
+        for t in range(new[s]):
+            r, pos = cu[s] + t, int(old[s]) + t
+            cache.write(own[s][pos // 16], pos % 16, kc[r], ke[r], vc[r], ve[r])
+    fp8mm.mxfp4_kv_append(k.cuda(), v.cuda(), dev, _i32(table), _i32(lengths), 16, cu_seqlens=_i32(cu))
+    assert torch.equal(dev.cpu(), cache.data)
+    got = fp8mm.mxfp4_kv_gather(dev, _i32(table), _i32(cu), 16, 64, cu[-1], starts=_i32(old.tolist()))
+    for x, codes, e in zip(got, (kc, vc), (ke, ve)):
+        assert torch.equal(x.cpu(), ref.value(codes, e).bfloat16()[:cu[-1]])
+
+
+@pytest.mark.parametrize("batch,new,hq", [(600, 2, 2), (600, 3, 8), (300, 6, 16)])
+def test_attention_of_many_ragged_sequences(batch, new, hq):
+    """Several sequences to a strip of the plan: ragged ones, some without rows; the last shape on the kernel for many rows."""
+    rng = np.random.default_rng(batch + new)
+    count = rng.integers(0, 2 * new + 1, batch)
+    count[:3] = 0
+    count[-1] = 5 * batch * new // 100 + 1
+    total = int(count.sum())
+    lengths = (count + rng.integers(0, 50, batch)).tolist()
+    lengths[7] = 700
+    cache, table, own = _filled(rng, lengths, 32, 1, 64, 12)
+    cu = np.concatenate([[0], np.cumsum(count)]).tolist()
+    q = _queries(total, hq, 64)
+    for ws in (_workspace(64), None):
+        out = fp8mm.mxfp4_kv_attention(q.cuda(), cache.data.cuda(), _i32(table), _i32(lengths), 32, cu_seqlens=_i32(cu), workspace=ws)
+        many = ws is not None and -(-total // batch) * hq >= 96
+        assert many == (ws is not None and hq == 16)
+        _check_attention(out, None, q, cache, own, lengths, cu, 0.125, BF16_WEIGHTS if many else 2.0 ** -10)
+
+
+@pytest.mark.parametrize("hq", [16, 128])
+def test_tables_wide_enough_for_coarse_units(hq):
+    """A page table with room for 2^31 tokens a sequence: the plan's units stand for several steps each."""
+    dim, hk, ps, batch = 64, 16, 4096, 2
+    most = (2 ** 31 - 1) // ps
+    lengths, rows = [5000, 9000], [1, 1]
+    k, v = _kv(sum(lengths), hk, dim, 3)
+    cache = torch.zeros(6, fp8mm.mxfp4_kv_page_bytes(ps, hk, dim), dtype=torch.uint8, device="cuda")
+    pages = [[4, 1], [0, 5, 2]]
+    wide = torch.full((batch, most), -1, dtype=torch.int32, device="cuda")
+    for s, p in enumerate(pages):
+        wide[s, :len(p)] = _i32(p)
+    narrow = wide[:, :3].contiguous()
+    cu = _i32([0, 5000, 14000])
+    fp8mm.mxfp4_kv_append(k.cuda(), v.cuda(), cache, wide, _i32(lengths), ps, cu_seqlens=cu)
+    got = fp8mm.mxfp4_kv_gather(cache, narrow, cu, ps, dim, 14000)
+    want = [ref.value(*ref.quantize(x)) for x in (k, v)]
+    assert all(torch.equal(a.cpu(), b.bfloat16()) for a, b in zip(got, want))
+    q = _queries(2, hq, dim)
+    steps, tiles = (2 ** 31 - 1) // 32 + 7, (2 * hq // hk / 4 + 2) * hk
+    assert steps * tiles > 2e9                                  # units of one step would pass 31 bits
+    for table in (wide, narrow):
+        out = fp8mm.mxfp4_kv_attention(q.cuda(), cache, table, _i32(lengths), ps, workspace=_workspace(dim)).double().cpu()
+        for s, (a, b) in enumerate(((0, 5000), (5000, 14000))):
+            w, mag, _ = ref.attention(q[s:s + 1], want[0][a:b], want[1][a:b], dim ** -0.5)
+            assert ((out[s:s + 1] - w).abs() <= 2.0 ** -8 * w.abs() + (2.0 ** -10 + 2.0 ** -16) * mag).all()
+
+
 def test_single_rows_and_heads_of_any_stride():
     """The stride of a dimension of one element says nothing: it is not checked."""
     dim, ps = 64, 16
@@ -117,6 +192,18 @@ def test_single_rows_and_heads_of_any_stride():
     layers = torch.arange(64, dtype=torch.uint8, device="cuda").view(1, 4, 16)
     fp8mm.kv_copy_pages(layers.as_strided(layers.shape, (5, 16, 1)), [0], [3])
     assert torch.equal(layers[0, 3], layers[0, 0])
+
+
+@pytest.mark.parametrize("new,hq,hk", [([1, 1, 1], 4, 2), ([1, 1, 1], 32, 2), ([70, 64, 70], 4, 2)])
+def test_results_over_the_queries(new, hq, hk):
+    dim, lengths = 64, [1500, 130, 800]
+    cache, table, own = _filled(np.random.default_rng(4), lengths, 16, hk, dim, 3)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q, dev, ws = _queries(cu[-1], hq, dim).cuda(), cache.data.cuda(), _workspace(dim)
+    args = (dev, _i32(table), _i32(lengths), 16, _i32(cu))
+    want = fp8mm.mxfp4_kv_attention(q, *args, workspace=ws)
+    got = fp8mm.mxfp4_kv_attention(q, *args, workspace=ws, out=q)
+    assert got is q and torch.equal(got, want)
 
 
 def test_error_words_of_both_kinds_are_kept():
