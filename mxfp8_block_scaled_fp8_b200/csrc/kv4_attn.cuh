@@ -555,6 +555,7 @@ struct AttnWarp {
           }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+        if constexpr (FOLD == 2) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));  // one maximum for both halves of a row
         const bool same = !(mx > m[t][k] + kSlack);
         const float mn = same ? m[t][k] : mx + kHead;
         r[t][k] = same ? 1.f : ex2(m[t][k] - mn);
@@ -626,20 +627,12 @@ struct AttnWarp {
     uint32_t low = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float own[2] = {1.f, 1.f}, other[2] = {0.f, 0.f};
       bool under[2] = {false, false};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[t][k] += __shfl_xor_sync(0xFFFFFFFFu, l[t][k], off);
-        if constexpr (FOLD == 2) {
-          const float om = __shfl_xor_sync(0xFFFFFFFFu, m[t][k], 2), ol = __shfl_xor_sync(0xFFFFFFFFu, l[t][k], 2);
-          const float mx = fmaxf(m[t][k], om);
-          own[k] = m[t][k] == -INFINITY ? 0.f : ex2(m[t][k] - mx);
-          other[k] = om == -INFINITY ? 0.f : ex2(om - mx);
-          m[t][k] = mx;
-          l[t][k] = l[t][k] * own[k] + ol * other[k];
-        }
+        if constexpr (FOLD == 2) l[t][k] += __shfl_xor_sync(0xFFFFFFFFu, l[t][k], 2);
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -649,7 +642,7 @@ struct AttnWarp {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float& y = o[t][j][k];
-            if constexpr (FOLD == 2) y = y * own[k & 1] + __shfl_xor_sync(0xFFFFFFFFu, y, 2) * other[k & 1];
+            if constexpr (FOLD == 2) y += __shfl_xor_sync(0xFFFFFFFFu, y, 2);
             top[k & 1] = fmaxf(top[k & 1], fabsf(y));
             y = scale2(y, ref(b) - 127 - kBias);
           }

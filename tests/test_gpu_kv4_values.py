@@ -263,3 +263,39 @@ def test_scales_of_any_size(dim, rows, scale):
                 kk, vv = (x[:n - rows + i + 1, h // group] for x in written[2])
                 # the call's scale is a float
                 _check_row(out[i, h], lse[i, h], q[i, h], kk, vv, float(np.float32(scale)), weights)
+
+
+def _scored(n, heads, dim, scores, sizes, seed=6):
+    """Keys whose scores under a query of ones in its first 32 elements are `scores` (natural units, scale 1, to 3 bits),
+    and values of magnitude `sizes`, by token."""
+    g = torch.Generator().manual_seed(seed)
+    k = 0.01 * torch.randn(n, heads, dim, generator=g)
+    k[..., :32] = (torch.tensor(scores) / 32).view(n, 1, 1)
+    v = torch.randn(n, heads, dim, generator=g) * torch.tensor(sizes).view(n, 1, 1)
+    return _written(k.bfloat16(), v.bfloat16())
+
+
+def _check_ones(written, rows, group, dim):
+    n, heads, _ = written[2][0].shape
+    q = 0.5 * torch.randn(rows, heads * group, dim, generator=torch.Generator().manual_seed(2))
+    q[..., :32] = 1.0
+    q = q.bfloat16()
+    for ws, weights in _kinds(rows, group, dim):
+        out, lse = _run(q, written, heads, 1.0, ws)
+        for i in range(rows):
+            for h in range(heads * group):
+                k, v = (x[:n - rows + i + 1, h // group] for x in written[2])
+                _check_row(out[i, h], lse[i, h], q[i, h], k, v, 1.0, weights)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,group", [(1, 1), (1, 4), (2, 4), (3, 5), (40, 3)])
+@pytest.mark.parametrize("huge,large", [(3, 54), (19, 38), (3, 38), (35, 54), (54, 3)])
+def test_huge_values_of_no_weight(dim, rows, group, huge, large):
+    """A token of values 2^40 whose score is 40 below that of another one (2^-58 of its weight), in either half of a step of
+    32 tokens, before it and after."""
+    n = 64 + rows - 1
+    scores, sizes = [-45.0] * n, [1.0] * n
+    scores[huge], sizes[huge] = -40.0, 2.0 ** 40
+    scores[large] = 0.0
+    _check_ones(_scored(n, 2, dim, scores, sizes), rows, group, dim)
