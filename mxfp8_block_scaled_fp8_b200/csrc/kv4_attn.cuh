@@ -235,7 +235,7 @@ constexpr float kHead = 2.f;   // to so far above it
 // Scores (log2) from this size on are taken one by one (step_slow): a fused x sc - m has the exact product, m a rounded
 // one, and the difference, half an ulp of the score, is below 2^-12 only under it.
 constexpr float kExact = 4096.f;
-constexpr int kSpare = 8;      // how far E_b may be above what the weights need, to take in the step's exponents
+constexpr int kSpare = 10;     // how far E_b may be above what the weights need, to take in the steps' exponents
 constexpr int kMinRef = 13;    // so that 2^(127 + kBias - E_b) is finite
 // A row's sums below this, in the units that its weights were rounded in, are not to be had from shared references: each
 // token is off by 6 * 2^-25 at most where its weight is below f16's normal range (weights of the row's largest score alone
@@ -262,6 +262,7 @@ struct AttnWarp {
   float limit[NT][2];          // (m + kSlack) / sc: raw scores above it move the maximum; -inf: all go the slow way
   float unit[NB];              // 2^(127 + kBias - E_b), which tells E_b (kMinRef and up)
   uint32_t ref_half;           // E_b / 2 in bytes, with the bytes' top bits set
+  uint32_t spare;              // how far E_b is above what the weights need, in bytes
   int vis[NT][2];              // tokens visible to columns 2 c, 2 c + 1; INT_MAX where the column is no row
   int vis_min;                 // least of them
 
@@ -345,6 +346,7 @@ struct AttnWarp {
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) set_ref(b, kMinRef);
+    spare = 0;
     vis_min = seen;
   }
 
@@ -579,17 +581,18 @@ struct AttnWarp {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int old = ref(b);
-      int e = max(old - drop, kMinRef), all = 0;
+      int need = max(old - static_cast<int>((spare >> (8 * b)) & 0xFFu) - drop, kMinRef), all = 0;
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int one = static_cast<int>((ve[u][h] >> (8 * b)) & 0xFFu);
-          e = max(e, one + top[u][h]);
+          need = max(need, one + top[u][h]);
           all = max(all, one);
         }
-      e = __reduce_max_sync(0xFFFFFFFFu, e);
-      e = max(e, min(e + kSpare, __reduce_max_sync(0xFFFFFFFFu, all)));
+      need = __reduce_max_sync(0xFFFFFFFFu, need);
+      const int e = max(need, min(need + kSpare, max(old, __reduce_max_sync(0xFFFFFFFFu, all))));
+      spare = (spare & ~(0xFFu << (8 * b))) | static_cast<uint32_t>(e - need) << (8 * b);
       set_ref(b, e);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {

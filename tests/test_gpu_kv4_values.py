@@ -299,3 +299,16 @@ def test_huge_values_of_no_weight(dim, rows, group, huge, large):
     scores[huge], sizes[huge] = -40.0, 2.0 ** 40
     scores[large] = 0.0
     _check_ones(_scored(n, 2, dim, scores, sizes), rows, group, dim)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,group", [(1, 1), (1, 4), (2, 4), (3, 5), (40, 3)])
+@pytest.mark.parametrize("size,score", [(2.0 ** -30, -22.0), (2.0 ** -20, -16.0), (2.0 ** -40, -28.0)])
+def test_a_large_weight_of_small_values(dim, rows, group, size, score):
+    """The first token has nearly all of the weight and values so small that the others', of 2^-23 to 2^-40 of its weight,
+    matter as much."""
+    n = 400
+    g = torch.Generator().manual_seed(1)
+    scores, sizes = (score + torch.rand(n, generator=g)).tolist(), [1.0] * n
+    scores[0], sizes[0] = 0.0, size
+    _check_ones(_scored(n, 2, dim, scores, sizes), rows, group, dim)
