@@ -340,7 +340,8 @@ fp8mm_status concat_mla_k(const void* k_nope, const void* k_rope, void* k_out, i
  *   y = x * rsqrt(mean(x^2) + eps) * w             (left out when both weights are NULL)
  *   (y[a], y[b]) <- (y[a] cos - y[b] sin, y[b] cos + y[a] sin)
  * over rot_dim / 2 pairs, pair i being (i, i + rot_dim / 2), or with interleaved != 0 (2 i, 2 i + 1);
- * elements from rot_dim on are not rotated.  fp32 throughout, rounded once to bf16.
+ * elements from rot_dim on are not rotated.  fp32 throughout, rounded once to bf16; the sum of squares too, so that a
+ * head's magnitudes have to be below 2^59 and, where eps is 0, above 2^-60.
  *   q, k         [tokens, heads, head_dim] bf16, strides in elements (q and k may be slices of one
  *                projection's output); q_out, k_out the same, and may be q and k themselves (in place); no
  *                other overlap
@@ -411,13 +412,17 @@ fp8mm_status mxfp4_kv_gather(const fp8mm_kv_cache* cache, const int32_t* starts,
  *   out[r, h] = sum_j softmax_j(scale <q[r, h], k[j, h / g]>) v[j, h / g],  j <= position of row r,
  * g = q_heads / kv_heads, row i of sequence s's n rows at position seq_lens[s] - n + i (append first, then
  * attend).  A row that sees no token (seq_lens[s] == 0, or a position below 0) gives zeros.  Scores, softmax
- * statistics and sums are fp32.  Queries enter as f16, scaled row by row so that their 8 bits are kept down to 2^-27
- * of the row's largest magnitude, and weights with 11 bits; but in a call with a workspace and 96 or more rows of a
- * key/value head per sequence (rows / batch, rounded up, times g) queries enter exactly and weights with 8 bits, and
- * products are bf16 (values past 2^100 may overflow there).  Which of the two a row gets goes by its call.  For few rows
- * blocks with e = 0 (magnitudes up to 6 * 2^-127) may count as zeros.  A NaN in a key makes the rows that see it NaN, in
- * a value the 32 elements of its block, or makes them 2^100 and more where the rows are many and not all rows of the
- * chunk see it; other rows are not touched.  Rows of a sequence with a page id outside the pool are unspecified.
+ * statistics and sums are fp32.  Two kernels, of which a row gets one by its call:
+ *   with a workspace and 96 or more rows of a key/value head per sequence (rows / batch, rounded up, times g): queries
+ *   enter exactly, weights with 8 bits, products are bf16 (values past 2^100 may overflow);
+ *   else: queries with their 8 bits down to 2^-27 of the row's largest magnitude (f16, scaled by row), weights with 11
+ *   bits, those that count for less than 2^-14 of the row's sum with an error of 2^-22 of it; blocks with e = 0
+ *   (magnitudes up to 6 * 2^-127) may count as zeros.
+ * The time goes by the call too: a batch of single tokens and a long chunk is faster as two (63 sequences of up to 8192
+ * tokens and a chunk of 512: 63 and 73 us apart, 275 in one).
+ * A NaN in a key makes the rows that see it NaN, in a value the 32 elements of its block, or makes them 2^100 and more
+ * where the rows are many and not all rows of the chunk see it; other rows are not touched.  Rows of a sequence with a
+ * page id outside the pool are unspecified.
  *   q    [rows, q_heads, head_dim] bf16;  out the same shape, strides in elements, 16-byte aligned; out may be q itself
  *   lse  NULL or [rows, q_heads] fp32, row stride lse_stride: log(sum_j exp(scale <q, k_j>)), -inf for an
  *        empty row

@@ -255,9 +255,14 @@ fp8mm_status mxfp4_kv_attention(const void* q_bf16, int64_t q_stride_t, int64_t 
   if (tiles > 1e9) return FP8MM_ERR_SHAPE;
   p.unit_steps = static_cast<int32_t>(std::min(1e9, 1 + steps * tiles / 2e9));
   // Rows that a sequence has on average decide the tile: 4, 8 or 16 of them, or 256 (which needs the workspace).
-  // 32 sequences of 4096 tokens, 8 heads: 4 rows 38.1 us in tiles of 4, 40.6 of 8, 56.4 of 16; 8 rows 41.6 in
-  // tiles of 8, 57.9 of 16.  16 such sequences: 64 rows 107 us in tiles of 16, 132 of 256; 96 rows 154 and 136;
-  // 128 rows 200 and 134; 256 rows 389 and 140.
+  // 32 sequences of 4096 tokens, 8 heads: 4 rows 39.1 us in tiles of 4, 41.4 of 8, 58.5 of 16; 8 rows 42.4 in
+  // tiles of 8, 60.5 of 16.  Tiles of 16 and of 256, head size 128 | 64, us in a graph:
+  //   16 sequences of 4096: 64 rows 111, 133 | 81, 120;  96 rows 158, 139 | 115, 125;  128 rows 206, 138 | 150, 118
+  //   64 of 512:            64 rows 183, 134 | 99, 104;  96 rows 268, 148 | 136, 115;  128 rows 327, 153 | 165, 111
+  //   1 of 32768:           64 rows 56, 70 | 42, 58;     96 rows 79, 70 | 57, 57;      128 rows 97, 67 | 70, 54
+  //   2 of 1024:            96 rows 23, 39 | 19, 28;     128 rows 24, 40 | 20, 28;     256 rows 34, 42 | 26, 29
+  // Little work in short contexts would be better off in tiles of 16 throughout, at most 16 us; one size serves a
+  // whole call, whatever its sequences' own rows.
   const int64_t tile = cdiv(rows, cache->batch) * p.group;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.partials != nullptr && tile >= kPreFrom)
@@ -364,8 +369,8 @@ fp8mm_status qk_norm_rope(const void* q_bf16, int64_t q_stride_t, int64_t q_stri
   p.max_pos = static_cast<int32_t>(max_pos);
   p.eps = eps;
   // warps of a token: one that walks all its heads, keeping the angles, and more, down to one step each, while the
-  // tokens alone would not fill the SMs (8192 tokens of 40 heads, before the steps were joined: 39.6 us with one
-  // warp, 42.9 with three)
+  // tokens alone would not fill the SMs (40 heads of 128, one warp and one per step: 8192 tokens 33.7 and 45.9 us, 2048
+  // tokens 11.3 and 10.9, 1024 tokens 8.8 and 6.2, 7.9 by this rule, 64 tokens 6.2 and 2.5)
   const int64_t step = kNormUnroll * (256 / head_dim), steps = cdiv(q_heads, step) + cdiv(k_heads, step);
   const int64_t fill = std::max<int64_t>(1, static_cast<int64_t>(dev.sms) * 32 / tokens);
   p.slices = static_cast<int32_t>(std::min(steps, fill));

@@ -290,8 +290,8 @@ __device__ __forceinline__ uint32_t load_exponents(const uint8_t* src) {
 // 16 for prompts.  Bound by HBM for long prompts (4 D bytes
 // in, 17 D / 16 bytes out per token and head; 8 prompts of 1 to 2047 tokens, 8
 // heads, written and read back: 23.4 us, 27.6 with the values' loads behind the
-// keys' conversion) and by the latency of the index loads for a decode step
-// (64 tokens 4.4 us).  A group that is written only in part keeps the
+// keys' conversion; 131072 tokens 124 us, 5.5 TB/s) and by the latency of the
+// index loads for a decode step (64 tokens 4.4 us).  A group that is written only in part keeps the
 // codes of its other tokens: values share bytes between neighbouring tokens,
 // so those words are merged with what the record held.
 template <int D, int kRows>
@@ -540,7 +540,7 @@ constexpr int kNormUnroll = 4;
 // query heads and once for its key heads, and partners exchange bf16 pairs.
 // fp32 throughout, rounded once.  Bound by HBM for long prompts (each element
 // read and written once), by latency for a decode step (64 tokens 2.5 us).
-// 8192 tokens of 40 heads of 128: 34.3 us, 4.9 TB/s; steps of 2 heads 41.8, of 4
+// 8192 tokens of 40 heads of 128: 33.4 us in a graph, 5.1 TB/s; steps of 2 heads 41.8, of 4
 // 37.0, of 16 42.0; weights and angles apart, fp32 partners 39.6.
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const QkNormArgs p) {

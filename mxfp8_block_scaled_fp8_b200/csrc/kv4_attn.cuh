@@ -18,12 +18,13 @@
 // guessed, and a captured graph follows the lengths in memory.
 // Bound by reading the cache, 17 D bytes per 16 tokens and head, once, and close
 // behind it by the conversions (two a clock and SM, 8 per record and lane of
-// each operand: the ALU pipe is 63 % busy).  Measured: 4 contexts of 100003 to
-// 131072 tokens, 32 heads on 8, 100 to 109 us on different cards, 77 to 71 % of
-// the rate of a copy; 64 of 1 to 8192 tokens 68 us, 64 %.  Measured on the way, the long contexts: eight warps
-// of a CTA on one piece, joined through shared memory, 117 us; the same with a
-// warp that brings the records and one that joins results, 122 us (a CTA waits
-// for its slowest warp).
+// each operand: the ALU pipe is about 60 % busy, HBM about 55 %; neither is
+// full).  Measured: 4 contexts of 100003 to 131072 tokens, 32 heads on 8, 100 to
+// 109 us a call on different cards, 77 to 71 % of the rate of a copy; 64 of 1 to
+// 8192 tokens 68 us, 64 %.  Measured on the way, the long contexts: eight warps of
+// a CTA on one piece, joined through shared memory, 117 us; the same with a warp
+// that brings the records and one that joins results, 122 us (a CTA waits for its
+// slowest warp).
 //
 // Matrix instructions on registers, not tcgen05: with 4 to 16 rows the product
 // is a hundredth of what the tensor cores give, and tcgen05 would want the codes
@@ -46,9 +47,9 @@
 // The rows of a tile share it.  A row whose sums come out small in its units
 // (kLow), since another row has met values far above what this one has, is taken
 // again by itself with its own: a token with huge values, seen by some of the
-// rows, leaves the others their bits.  (64 sequences of 1 to 8192 tokens 65.6 us in
-// a graph, 64.8 without that look at the sums; references by row, which cost
-// multiplications and registers in every step, 69 to 73 us.)
+// rows, leaves the others their bits.  (That look at the sums takes 0.8 us of 64
+// sequences of 1 to 8192 tokens, 66.0 us in a graph; references by row, which cost
+// multiplications and registers in every step, took 4 to 8.)
 #pragma once
 
 #include <climits>
@@ -148,7 +149,7 @@ __device__ __forceinline__ float scale2(float x, int n) {
 
 // What laying a tile out costs a warp, in steps (each short tile of a batch
 // adds its latency: queries, page table, first records, results).  64 sequences
-// of 1 to 8192 tokens: 92.6 us with 2, 73.6 with 4, 68.3 with 6, 68.8 with 10.
+// of 1 to 8192 tokens, in a graph: 74.6 us with 4, 66.9 with 6 (66.0 since), 66.9 with 10.
 constexpr int kTileSteps = 6;
 
 struct AttnSeq {

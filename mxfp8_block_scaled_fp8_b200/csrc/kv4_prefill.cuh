@@ -21,12 +21,15 @@
 // Bounds of a step (256 rows, D = 128), in SM clocks: tensor 1290 (PV 8 x 64;
 // QK 16 x 48.6, because its operands' 6 KB pass shared memory at 128 bytes a
 // clock), exponentials 1024, writing tiles 400 of shared memory's clocks.
+// At D = 64 a step has half the products and the same exponentials, 1024 clocks,
+// which bound it: two chunks of 2048 tokens at 16384 take 937 us, 432 of them
+// exponentials.
 // Measured on two prompts' chunks of 1025 to 2048 tokens in contexts of up to
-// 16384, 32 heads on 8 (541 GFLOP): 618 us, 875 TFLOP/s, 53 % of the rate that a
-// plain bf16 GEMM reaches here; without the conversion to bf16 it would be 546,
-// without the exponentials 598, without both 500: what is left is the tensor pipe
-// beside the softmax's reads and writes of TMEM.  What was tried on the way,
-// same work: steps of 128 tokens with one place for scores 871 us (the softmax
+// 16384, 32 heads on 8 (541 GFLOP): 621 us in a graph, 871 TFLOP/s, 53 % of the
+// rate that a plain bf16 GEMM reaches here (626 to 632 a call); when it took 618,
+// it was 546 without the conversion to bf16, 598 without the exponentials, 500
+// without both: what is left is the tensor pipe beside the softmax's reads and
+// writes of TMEM.  What was tried on the way, same work: steps of 128 tokens with one place for scores 871 us (the softmax
 // waits for its own products); scores in two places but tiles of 128 tokens
 // freed whole 918 us (conversion in the chain); steps of 128 tokens whose
 // products are issued as they are ready 713 us; one issuing warp 627 us (its
@@ -53,8 +56,8 @@ constexpr float kPreSlack = 8.f;
 // step is searched (pre_search).
 constexpr float kPreExact = 16777216.f;
 // What a tile costs beside its tokens, in units of 64 tokens (queries to shared
-// memory, the chain's fill and drain, the rows' store): 644 us with 6, 618 with
-// 8, 619 with 11.
+// memory, the chain's fill and drain, the rows' store): 665 us with 6, 630 with
+// 8, 621 with 9, 624 with 11.
 constexpr int kPreTileCost = 9;
 constexpr uint32_t kIdescBf16 = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 4 << 24);
 
