@@ -29,11 +29,12 @@
 // rate that a plain bf16 GEMM reaches here (626 to 632 a call); when it took 618,
 // it was 546 without the conversion to bf16, 598 without the exponentials, 500
 // without both: what is left is the tensor pipe beside the softmax's reads and
-// writes of TMEM.  What was tried on the way, same work: steps of 128 tokens with one place for scores 871 us (the softmax
-// waits for its own products); scores in two places but tiles of 128 tokens
-// freed whole 918 us (conversion in the chain); steps of 128 tokens whose
-// products are issued as they are ready 713 us; one issuing warp 627 us (its
-// waits are the tensor pipe's); four warps for values and two for keys 677 us.
+// writes of TMEM.  What was tried on the way, same work: steps of 128 tokens with
+// one place for scores 871 us (the softmax waits for its own products); scores in
+// two places but tiles of 128 tokens freed whole 918 us (conversion in the chain);
+// steps of 128 tokens whose products are issued as they are ready 713 us; one
+// issuing warp 627 us (its waits are the tensor pipe's); four warps for values and
+// two for keys 677 us.
 //
 // Work split: as in kv4_attn.cuh, a job per CTA in a line of costs, which here
 // follow the causal mask; cut tiles are joined by the same second kernel.

@@ -488,8 +488,8 @@ def _kv_cache(cache, page_table, page_size: int, head_dim: int, dev: int):
     if one <= 0 or size % one != 0 or size == 0:
         raise ValueError(f"cache: pages of {size} bytes do not hold {page_size} tokens of whole heads of {head_dim}")
     return size // one, batch, KV_CACHE_DESC.pack(
-        cache.data_ptr(), cache.stride(0) if pages > 1 else size, pages, page_size, size // one, head_dim, page_table.data_ptr(),
-        page_table.stride(0) if batch > 1 else most, most, batch)
+        cache.data_ptr(), cache.stride(0) if pages > 1 else size, pages, page_size, size // one, head_dim,
+        page_table.data_ptr(), page_table.stride(0) if batch > 1 else most, most, batch)
 
 
 def mxfp4_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
@@ -609,7 +609,8 @@ def kv_copy_pages(cache: torch.Tensor, src, dst, stream=None) -> torch.Tensor:
         raise ValueError(f"page ids: {e}") from None
     at = ctypes.cast(ids, _P).value
     size = cache.element_size()
-    layers, layer_stride = (shape[0], st[0] * size) if len(shape) == 3 and shape[0] > 1 else (len(shape) == 2 or shape[0], 0)
+    layers = shape[0] if len(shape) == 3 else 1
+    layer_stride = st[0] * size if layers > 1 else 0
     _check("kv_copy_pages", lib().kv_copy_pages(cache.data_ptr(), shape[-2], shape[-1] * size, st[-2] * size, layers,
                                                 layer_stride, at, at + 4 * n, n, _raw(dev)))
     return cache
