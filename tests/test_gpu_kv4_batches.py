@@ -1,6 +1,7 @@
 """Batches of the cache operators: bounds that do not begin at row 0, lengths
 that do not fit, many sequences, tables wider than 32 bits of work, single rows
-of any stride, results over the queries, workspaces that were not zeroed.
+of any stride, results over the queries, workspaces that were not zeroed, calls
+at once on several streams.
 Tolerances are those of tests/test_gpu_kv4.py."""
 import numpy as np
 import pytest
@@ -260,3 +261,43 @@ def test_workspaces_that_were_not_zeroed(new, hq, hk, fill):
     for _ in range(2):
         out = fp8mm.mxfp4_kv_attention(*args, workspace=ws)
         _check_attention(out, None, q, cache, own, lengths, cu, dim ** -0.5, BF16_WEIGHTS if new[0] > 1 else 2.0 ** -10)
+
+
+def test_calls_at_once_on_several_streams():
+    """Attention of few and of many rows, each with its own workspace, norms, a product and an append into another cache,
+    at once on four streams: the same bits as one after the other."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    jobs = []
+    for dim, hq, hk, new, length in ((64, 8, 2, 70, 2000), (128, 8, 2, 1, 3000)):
+        batch, ps = 3, 64
+        per = -(-length // ps)
+        cache = torch.zeros(batch * per, fp8mm.mxfp4_kv_page_bytes(ps, hk, dim), dtype=torch.uint8, device="cuda")
+        table = _i32(torch.randperm(batch * per, generator=torch.Generator().manual_seed(1)).view(batch, per).tolist())
+        lens, rows = _i32([length, length - 700, 65]), [0, length, 2 * length - 700, 2 * length - 635]
+        k, v, q = randn(rows[-1], hk, dim), randn(rows[-1], hk, dim), randn(new * batch, hq, dim)
+        cu, ws, other = _i32([i * min(new, 65) for i in range(batch + 1)]), _workspace(dim), torch.zeros_like(cache)
+        fp8mm.mxfp4_kv_append(k, v, cache, table, lens, ps, _i32(rows))
+        out, cu_rows = torch.zeros_like(q), _i32(rows)
+        jobs.append(lambda s, a=(q, cache, table, lens, ps, cu), o=out, w=ws: fp8mm.mxfp4_kv_attention(*a, out=o, workspace=w, stream=s))
+        jobs.append(lambda s, a=(k, v, other, table, lens, ps, cu_rows): fp8mm.mxfp4_kv_append(*a, stream=s))
+    x, cs, pos = randn(4096, 10, 128), torch.randn(4096, 128, device="cuda"), torch.arange(4096, dtype=torch.int32, device="cuda")
+    qo, ko = torch.zeros_like(x[:, :8]), torch.zeros_like(x[:, 8:])
+    jobs.append(lambda s: fp8mm.qk_norm_rope(x[:, :8], x[:, 8:], cs, pos, q_out=qo, k_out=ko, stream=s)[0])
+    a, b = fp8mm.mxfp8_quantize(randn(512, 1024)), fp8mm.mxfp8_quantize(randn(1024, 1024))
+    c = torch.zeros(512, 1024, dtype=torch.bfloat16, device="cuda")
+    jobs.append(lambda s: fp8mm.mxfp8_gemm(*a, *b, c=c, stream=s))
+    results, want = [], []
+    for job in jobs:
+        results.append(job(torch.cuda.current_stream()))
+        torch.cuda.synchronize()
+        want.append(results[-1].clone())
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(8):
+        for r in results:
+            r.zero_()
+        torch.cuda.synchronize()
+        for i, job in enumerate(jobs * 3):                     # a job stays on its stream
+            job(streams[i % len(jobs) % 4])
+        torch.cuda.synchronize()
+        assert all(torch.equal(r, w) for r, w in zip(results, want))
